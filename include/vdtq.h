@@ -362,6 +362,121 @@ int qgemm_mx_quant(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
                    int64_t M, int64_t N, int64_t K, void* stream);
 
 /*
+ * rmsnorm_quantize -- the norm in front of a block's linears: residual
+ * addition, root-mean-square norm, block Hadamard transform and
+ * quantization of bf16 rows in one pass.
+ *
+ * Defined by: [gist] §2.A (block Hadamard before quantization) and §4 /
+ * [yly] §四 (quantization fused with the kernel that produces its input).
+ *
+ * Per row of K elements (RN: fp32 round-to-nearest-even):
+ *   r   = bf16_RNE(RN(x + residual)), or x without a residual;
+ *   inv = RN(1 / sqrt(sum r^2 / K + eps)), sum, root and quotient in fp64;
+ *   y   = RN(RN(r * inv) * weight), or RN(r * inv) without a weight;
+ * then the butterflies, normalisation (one fp32 multiplication by
+ * RN(1/sqrt(had_block))) and INT8, BF16, MXFP4 or MXFP8 conversion of
+ * hadamard_quantize on y.
+ * A row with a NaN or an infinity in r is marked whole: BF16 writes NaNs,
+ * INT8 the scale NaN and codes 0, MX the scale byte 0xFF (NaN) and codes 0,
+ * so its products are NaN; the other rows are not affected.
+ *
+ * x_dev          bf16 [M][ldx], ldx >= K, a multiple of 8
+ * M              rows, >= 0 (0 is a no-op)
+ * K              columns, > 0, <= 16384, a multiple of 16 and of had_block;
+ *                for MXFP4 / MXFP8 a multiple of 32
+ * residual_dev   bf16 [M][ldr] (ldr as ldx) or NULL
+ * weight_dev     float [K] or NULL (ones); finite
+ * eps            > 0, finite
+ * had_block      16, 32, 64, 128 or 256
+ * fmt            VDTQ_FMT_INT8, VDTQ_FMT_BF16, VDTQ_FMT_MXFP4 or
+ *                VDTQ_FMT_MXFP8 (NVFP4 needs the whole tensor's maximum
+ *                first: VDTQ_EUNSUPPORTED)
+ * sum_dev        bf16 [M][lds] (lds as ldx), receives r; NULL: not written.
+ *                Needs a residual.  It may be x or the residual itself (same
+ *                address and row stride); any other overlap of the outputs
+ *                with an input is refused
+ * q_dev          INT8: int8 [M][K]; BF16: bf16 [M][K]; MXFP4: uint8
+ *                [M][K/2]; MXFP8: uint8 E4M3 [M][K]; 16-byte aligned
+ * scales_dev     INT8: float [M]; MXFP4, MXFP8: uint8 E8M0 [M][K/32]; BF16:
+ *                ignored, may be NULL
+ * No workspace.  Errors: VDTQ_EINVAL for null or misaligned pointers, bad
+ * sizes, eps, had_block or fmt, or overlapping buffers; VDTQ_EUNSUPPORTED
+ * for K > 16384 or NVFP4.
+ */
+int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
+                     const void* residual_dev, int64_t ldr,
+                     const float* weight_dev, float eps, int had_block,
+                     int fmt, void* sum_dev, int64_t lds, void* q_dev,
+                     void* scales_dev, void* stream);
+
+/*
+ * qgemv_w4a16, qgemv_w4a8, qgemv_mx -- qgemm_w4a16, qgemm_w4a8 and qgemm_mx
+ * for at most VDTQ_GEMV_MAX_ROWS rows: modulation and timestep linears
+ * (rows = samples), single rows.  Same operands, layouts and results up to
+ * the order of the fp32 sums; every product is exact and added in fp32
+ * (qgemv_mx too: unlike qgemm_mx, it does not use the block-scaled matrix
+ * instruction, whose E4M3 x E2M1 sums drop low bits).
+ *
+ * Defined by: [gist] §4 / [yly] §四 (4-bit weights in every linear), with
+ * the activations of [gist] §2.A and §2.C.
+ *
+ * Operands as for the call of the same name, except: M <=
+ * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); scales
+ * need no alignment; N * K / 2 has no limit below the memory's.
+ * No workspace.  A NaN in an activation row, in its scale (INT8) or an
+ * 0xFF scale byte (MX) makes that row of Y NaN and no other.
+ * Errors: VDTQ_EINVAL for null or misaligned pointers, bad sizes or
+ * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS.
+ */
+#define VDTQ_GEMV_MAX_ROWS 32
+int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev,
+                const uint8_t* w_s_dev, const float* w_ts_dev,
+                const float* bias_dev, void* y_dev, int64_t ldy,
+                int out_dtype, int64_t M, int64_t N, int64_t K, void* stream);
+int qgemv_w4a8(const int8_t* a_q_dev, const float* a_s_dev,
+               const uint8_t* w_q_dev, const uint8_t* w_s_dev,
+               const float* w_ts_dev, const float* bias_dev, void* y_dev,
+               int64_t ldy, int out_dtype, int64_t M, int64_t N, int64_t K,
+               void* stream);
+int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
+             const uint8_t* w_q_dev, const uint8_t* w_s_dev,
+             const float* bias_dev, void* y_dev, int64_t ldy, int out_dtype,
+             int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * qgemm_mx_grouped -- qgemm_mx with weights per group of rows: rows
+ * offsets[e] .. offsets[e+1] - 1 of A are multiplied with the weights of
+ * expert e (text rows and video rows of one sequence with weights of their
+ * own; routed experts, rows sorted by expert).  Row counts are ragged and
+ * may be zero; they are read on the device, so a graph that holds the call
+ * replays with other counts.
+ *
+ * Defined by: [gist] §2.A / §3.1 and §4 as for qgemm_mx.
+ *
+ * a_fmt          VDTQ_FMT_MXFP4 or VDTQ_FMT_MXFP8
+ * a_q_dev, a_s_dev  [T] rows as for qgemm_mx
+ * w_q_dev        uint8 [E][N][K/2] E2M1 codes, w_s_dev uint8 E8M0
+ *                [E][N][K/32]: hadamard_quantize of the E * N stacked rows
+ * bias_dev       float [E][N] or NULL
+ * offsets_dev    int32 [E+1], not decreasing, 0 <= offsets[0],
+ *                offsets[E] <= T.  Other values give unspecified rows of Y
+ *                but reach nothing outside the buffers: each is taken as
+ *                the largest up to there, clamped to [0, T]
+ * y_dev          out_dtype [T][ldy]; rows before offsets[0] and from
+ *                offsets[E] on are left as they were
+ * T, N, E        >= 0 (T, N or E of 0 is a no-op); E <= 65536
+ * K              > 0, multiple of 32
+ * No workspace.
+ * Errors: VDTQ_EINVAL for a bad a_fmt or size, null or misaligned pointers,
+ * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128.
+ */
+int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
+                     const uint8_t* w_q_dev, const uint8_t* w_s_dev,
+                     const float* bias_dev, const int32_t* offsets_dev,
+                     int64_t E, void* y_dev, int64_t ldy, int out_dtype,
+                     int64_t T, int64_t N, int64_t K, void* stream);
+
+/*
  * block_stats -- one pass over a block's input, output and cached delta.
  *
  * Defined by: [gist] §2.A (Gamma_{t-1}: relative input-output difference of

@@ -100,3 +100,21 @@ def w4a8_group_partials(a_q, w_q) -> np.ndarray:
     ag = a.reshape(M, K // GROUP, GROUP)
     cg = c.reshape(N, K // GROUP, GROUP)
     return np.einsum("mgk,ngk->mng", ag, cg)
+
+
+def qgemm_mx_grouped(a_q, a_s, a_fmt, w_q, w_s, offsets, bias=None):
+    """Rows offsets[e] .. offsets[e+1] - 1 times expert e's weights (w stacked
+    to E * N rows; bias [E, N]).  Returns (float64 Y [T, N], covered rows):
+    rows outside every group are zero and not covered."""
+    E = len(offsets) - 1
+    N = w_q.shape[0] // E
+    y = np.zeros((a_q.shape[0], N))
+    covered = np.zeros(a_q.shape[0], bool)
+    for e in range(E):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        if r.stop <= r.start:
+            continue
+        w = slice(e * N, (e + 1) * N)
+        y[r], _ = qgemm_mx(a_q[r], a_s[r], a_fmt, w_q[w], w_s[w], None if bias is None else bias[e], "f32")
+        covered[r] = True
+    return y, covered

@@ -17,10 +17,12 @@ AMAX_GIVEN, STATS, GELU = 1, 2, 4
 ACT_SKIP, ACT_NVFP4, ACT_INT8, ACT_BF16 = 0, 1, 2, 3
 OP_HADAMARD_QUANTIZE, OP_BLOCK_STATS, OP_QGEMM = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 8 << 20      # VDTQ_NOALLOC_SCRATCH_BYTES
+GEMV_MAX_ROWS = 32                   # VDTQ_GEMV_MAX_ROWS
 
 # every extern "C" symbol include/vdtq.h declares
 EXPORTED = ["vdtq_last_error", "vdtq_version", "vdtq_workspace_bytes", "hadamard_quantize", "hadamard_quantize_noalloc",
-            "qgemm_w4a4", "qgemm_w4a8", "qgemm_w4a16", "qgemm_mx", "qgemm_mx_quant", "block_stats", "block_stats_mx8", "dmpq_state_init", "dmpq_step", "dmpq_budget_gamma", "dmpq_depth_params",
+            "qgemm_w4a4", "qgemm_w4a8", "qgemm_w4a16", "qgemm_mx", "qgemm_mx_quant", "rmsnorm_quantize",
+            "qgemv_w4a16", "qgemv_w4a8", "qgemv_mx", "qgemm_mx_grouped", "block_stats", "block_stats_mx8", "dmpq_state_init", "dmpq_step", "dmpq_budget_gamma", "dmpq_depth_params",
             "vdtq_outlier_ratio"]
 
 
@@ -45,8 +47,8 @@ class VdtqError(RuntimeError):
 _lib = None
 _lock = threading.Lock()
 
-vp, i64, sz, u32, i32, dbl = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint,
-                              ctypes.c_int, ctypes.c_double)
+vp, i64, sz, u32, i32, dbl, flt = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint,
+                                   ctypes.c_int, ctypes.c_double, ctypes.c_float)
 
 
 def lib() -> ctypes.CDLL:
@@ -79,6 +81,16 @@ def lib() -> ctypes.CDLL:
             L.qgemm_mx_quant.argtypes = [i32, vp, vp, vp, vp, vp, i32, i32, u32, vp, vp, i64, i64, i64, vp]
             L.qgemm_w4a8.restype = i32
             L.qgemm_w4a8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, vp, sz, vp]
+            L.rmsnorm_quantize.restype = i32
+            L.rmsnorm_quantize.argtypes = [vp, i64, i64, i64, vp, i64, vp, flt, i32, i32, vp, i64, vp, vp, vp]
+            L.qgemv_w4a16.restype = i32
+            L.qgemv_w4a16.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, vp]
+            L.qgemv_w4a8.restype = i32
+            L.qgemv_w4a8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, vp]
+            L.qgemv_mx.restype = i32
+            L.qgemv_mx.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, vp]
+            L.qgemm_mx_grouped.restype = i32
+            L.qgemm_mx_grouped.argtypes = [i32, vp, vp, vp, vp, vp, vp, i64, vp, i64, i32, i64, i64, i64, vp]
             L.block_stats_mx8.restype = i32
             L.block_stats_mx8.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
             L.block_stats.restype = i32

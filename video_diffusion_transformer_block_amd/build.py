@@ -23,8 +23,8 @@ LIB = os.path.join(HERE, "libvdtq.so")
 # plain streaming passes the benchmark times as ceilings (not the library's ABI)
 BENCH_LIB = os.path.join(HERE, "libvdtq_bench.so")
 BENCH_SOURCES = ["bench_stream.hip"]
-SOURCES = ["hadamard_quantize.hip", "qgemm.hip", "qgemm_mx.hip", "qgemm_w4a16.hip", "block_stats.hip", "api.cpp",
-           "dmpq.cpp"]
+SOURCES = ["hadamard_quantize.hip", "qgemm.hip", "qgemm_mx.hip", "qgemm_w4a16.hip", "block_stats.hip",
+           "rmsnorm_quantize.hip", "qgemv.hip", "api.cpp", "dmpq.cpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -257,6 +257,155 @@ int qgemm_mx_quant(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, co
   return hip_status(e, "qgemm_mx_quant launch");
 }
 
+// Whether two row-major [M][K] 2-byte arrays share an element.
+static bool rows_overlap(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t M, int64_t K) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t an = a + 2 * ((uintptr_t)(M - 1) * ldp + K), bn = b + 2 * ((uintptr_t)(M - 1) * ldq + K);
+  if (an <= b || bn <= a) return false;
+  if (ldp != ldq) return true;
+  // same stride: columns of one wider array are disjoint
+  const uintptr_t w = 2 * (uintptr_t)ldp, d = a > b ? (a - b) % w : (w - (b - a) % w) % w;
+  return d < 2 * (uintptr_t)K || d > w - 2 * (uintptr_t)K;
+}
+
+static bool bytes_overlap(const void* p, int64_t pn, const void* q, int64_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + (uintptr_t)qn && b < a + (uintptr_t)pn;
+}
+
+int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx, const void* residual_dev, int64_t ldr,
+                     const float* weight_dev, float eps, int had_block, int fmt, void* sum_dev, int64_t lds,
+                     void* q_dev, void* scales_dev, void* stream) {
+  const char* name = "rmsnorm_quantize";
+  if (M < 0 || M > kI32) return fail(VDTQ_EINVAL, "%s: M=%lld out of range", name, (long long)M);
+  if (had_block != 16 && had_block != 32 && had_block != 64 && had_block != 128 && had_block != 256)
+    return fail(VDTQ_EINVAL, "%s: had_block=%d must be 16, 32, 64, 128 or 256", name, had_block);
+  if (K <= 0 || K > kI32 || K % had_block)
+    return fail(VDTQ_EINVAL, "%s: K=%lld must be a positive multiple of had_block=%d", name, (long long)K, had_block);
+  if (fmt == VDTQ_FMT_NVFP4)
+    return fail(VDTQ_EUNSUPPORTED, "%s: NVFP4 needs the tensor maximum before any code (use hadamard_quantize)", name);
+  if (fmt != VDTQ_FMT_INT8 && fmt != VDTQ_FMT_BF16 && fmt != VDTQ_FMT_MXFP4 && fmt != VDTQ_FMT_MXFP8)
+    return fail(VDTQ_EINVAL, "%s: fmt=%d", name, fmt);
+  const bool mx = fmt == VDTQ_FMT_MXFP4 || fmt == VDTQ_FMT_MXFP8;
+  if (mx && K % 32) return fail(VDTQ_EINVAL, "%s: MX formats need K=%lld to be a multiple of 32", name, (long long)K);
+  if (!(eps > 0.0f) || eps > 3.0e38f) return fail(VDTQ_EINVAL, "%s: eps=%g must be positive and finite", name, (double)eps);
+  if (ldx < K || ldx % 8) return fail(VDTQ_EINVAL, "%s: ldx=%lld must be >= K and a multiple of 8", name, (long long)ldx);
+  if (residual_dev && (ldr < K || ldr % 8))
+    return fail(VDTQ_EINVAL, "%s: ldr=%lld must be >= K and a multiple of 8", name, (long long)ldr);
+  if (sum_dev && !residual_dev) return fail(VDTQ_EINVAL, "%s: sum without a residual", name);
+  if (sum_dev && (lds < K || lds % 8))
+    return fail(VDTQ_EINVAL, "%s: lds=%lld must be >= K and a multiple of 8", name, (long long)lds);
+  if (K > 16384) return fail(VDTQ_EUNSUPPORTED, "%s: rows longer than 16384 (K=%lld)", name, (long long)K);
+  if (M == 0) return ok();
+  if (!x_dev || !q_dev || (fmt != VDTQ_FMT_BF16 && !scales_dev)) return fail(VDTQ_EINVAL, "%s: null x/q/scales", name);
+  if (!aligned(x_dev, 16) || !aligned(residual_dev, 16) || !aligned(weight_dev, 16) || !aligned(sum_dev, 16) ||
+      !aligned(q_dev, 16) || (fmt != VDTQ_FMT_BF16 && !aligned(scales_dev, 4)))
+    return fail(VDTQ_EINVAL, "%s: x, residual, weight, sum and q must be 16-byte aligned, scales 4-byte aligned", name);
+  // a workgroup writes its rows of the outputs while others still read theirs
+  if (sum_dev && ((rows_overlap(sum_dev, lds, x_dev, ldx, M, K) && !(sum_dev == x_dev && lds == ldx)) ||
+                  (rows_overlap(sum_dev, lds, residual_dev, ldr, M, K) && !(sum_dev == residual_dev && lds == ldr))))
+    return fail(VDTQ_EINVAL, "%s: sum overlaps x or the residual without being it", name);
+  const int64_t qb = fmt == VDTQ_FMT_BF16 ? 2 * M * K : fmt == VDTQ_FMT_MXFP4 ? M * K / 2 : M * K;
+  const int64_t sb = fmt == VDTQ_FMT_BF16 ? 0 : mx ? M * (K / 32) : 4 * M;
+  const void* outs[2] = {q_dev, sb ? scales_dev : nullptr};
+  const int64_t outb[2] = {qb, sb};
+  for (int i = 0; i < 2; ++i) {
+    if (!outs[i]) continue;
+    if (bytes_overlap(outs[i], outb[i], x_dev, 2 * ((M - 1) * ldx + K)) ||
+        (residual_dev && bytes_overlap(outs[i], outb[i], residual_dev, 2 * ((M - 1) * ldr + K))) ||
+        (sum_dev && bytes_overlap(outs[i], outb[i], sum_dev, 2 * ((M - 1) * lds + K))) ||
+        (weight_dev && bytes_overlap(outs[i], outb[i], weight_dev, 4 * K)))
+      return fail(VDTQ_EINVAL, "%s: q or scales overlap another buffer", name);
+  }
+  if (sb && bytes_overlap(q_dev, qb, scales_dev, sb)) return fail(VDTQ_EINVAL, "%s: q overlaps scales", name);
+  if (sum_dev && weight_dev && bytes_overlap(sum_dev, 2 * ((M - 1) * lds + K), weight_dev, 4 * K))
+    return fail(VDTQ_EINVAL, "%s: sum overlaps weight", name);
+  hipError_t e = vdtq::launch_rmsnorm_quantize(x_dev, M, K, ldx, residual_dev, ldr, weight_dev, eps, had_block, fmt,
+                                               sum_dev, lds, q_dev, scales_dev, static_cast<hipStream_t>(stream));
+  return hip_status(e, "rmsnorm_quantize launch");
+}
+
+// The checks the few-row and grouped products share; kmul: K's granule.
+static int small_check(const char* name, const void* a_q, const void* a_s, const void* w_q, const void* w_s,
+                       const float* bias, const void* y, int64_t ldy, int out_dtype, int64_t M, int64_t N, int64_t K,
+                       int kmul) {
+  if (M < 0 || M > kI32 || N < 0 || N > kI32) return fail(VDTQ_EINVAL, "%s: M=%lld N=%lld out of range", name, (long long)M, (long long)N);
+  if (K <= 0 || K > kI32 - 4096 || K % kmul)
+    return fail(VDTQ_EINVAL, "%s: K=%lld must be a positive multiple of %d", name, (long long)K, kmul);
+  if (out_dtype != VDTQ_OUT_BF16 && out_dtype != VDTQ_OUT_F32) return fail(VDTQ_EINVAL, "%s: out_dtype=%d", name, out_dtype);
+  if (ldy < N) return fail(VDTQ_EINVAL, "%s: ldy=%lld < N=%lld", name, (long long)ldy, (long long)N);
+  if (M == 0 || N == 0) return VDTQ_OK;
+  if (!a_q || !a_s || !w_q || !w_s || !y) return fail(VDTQ_EINVAL, "%s: null pointer argument", name);
+  if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(y, out_dtype ? 4 : 2) || (bias && !aligned(bias, 4)))
+    return fail(VDTQ_EINVAL, "%s: misaligned pointer (codes need 16 bytes)", name);
+  return VDTQ_OK;
+}
+
+static int gemv_rows(const char* name, int64_t M) {
+  if (M > VDTQ_GEMV_MAX_ROWS)
+    return fail(VDTQ_EUNSUPPORTED, "%s: M=%lld is more than %d rows", name, (long long)M, VDTQ_GEMV_MAX_ROWS);
+  return VDTQ_OK;
+}
+
+int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev, const uint8_t* w_s_dev, const float* w_ts_dev,
+                const float* bias_dev, void* y_dev, int64_t ldy, int out_dtype, int64_t M, int64_t N, int64_t K,
+                void* stream) {
+  const char* name = "qgemv_w4a16";
+  int rc = small_check(name, a_dev, a_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
+  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (M == 0 || N == 0) return ok();
+  if (!w_ts_dev || !aligned(w_ts_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned w_ts", name);
+  hipError_t e = vdtq::launch_qgemv(0, a_dev, nullptr, w_q_dev, w_s_dev, w_ts_dev, bias_dev, y_dev, ldy, out_dtype, M,
+                                    N, K, static_cast<hipStream_t>(stream));
+  return hip_status(e, "qgemv_w4a16 launch");
+}
+
+int qgemv_w4a8(const int8_t* a_q_dev, const float* a_s_dev, const uint8_t* w_q_dev, const uint8_t* w_s_dev,
+               const float* w_ts_dev, const float* bias_dev, void* y_dev, int64_t ldy, int out_dtype, int64_t M,
+               int64_t N, int64_t K, void* stream) {
+  const char* name = "qgemv_w4a8";
+  int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
+  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (M == 0 || N == 0) return ok();
+  if (!w_ts_dev || !aligned(w_ts_dev, 4) || !aligned(a_s_dev, 4))
+    return fail(VDTQ_EINVAL, "%s: null w_ts or misaligned w_ts / a_s", name);
+  hipError_t e = vdtq::launch_qgemv(1, a_q_dev, a_s_dev, w_q_dev, w_s_dev, w_ts_dev, bias_dev, y_dev, ldy, out_dtype,
+                                    M, N, K, static_cast<hipStream_t>(stream));
+  return hip_status(e, "qgemv_w4a8 launch");
+}
+
+int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, const uint8_t* w_q_dev,
+             const uint8_t* w_s_dev, const float* bias_dev, void* y_dev, int64_t ldy, int out_dtype, int64_t M,
+             int64_t N, int64_t K, void* stream) {
+  const char* name = "qgemv_mx";
+  if (a_fmt != VDTQ_FMT_MXFP4 && a_fmt != VDTQ_FMT_MXFP8) return fail(VDTQ_EINVAL, "%s: a_fmt=%d", name, a_fmt);
+  int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 32);
+  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (M == 0 || N == 0) return ok();
+  hipError_t e = vdtq::launch_qgemv(a_fmt == VDTQ_FMT_MXFP8 ? 2 : 3, a_q_dev, a_s_dev, w_q_dev, w_s_dev, nullptr,
+                                    bias_dev, y_dev, ldy, out_dtype, M, N, K, static_cast<hipStream_t>(stream));
+  return hip_status(e, "qgemv_mx launch");
+}
+
+int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, const uint8_t* w_q_dev,
+                     const uint8_t* w_s_dev, const float* bias_dev, const int32_t* offsets_dev, int64_t E, void* y_dev,
+                     int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, void* stream) {
+  const char* name = "qgemm_mx_grouped";
+  if (a_fmt != VDTQ_FMT_MXFP4 && a_fmt != VDTQ_FMT_MXFP8) return fail(VDTQ_EINVAL, "%s: a_fmt=%d", name, a_fmt);
+  if (E < 0 || E > 65536) return fail(VDTQ_EINVAL, "%s: E=%lld out of range", name, (long long)E);
+  if (E == 0) T = 0;
+  int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, T, N, K, 32);
+  if (rc) return rc;
+  if (T == 0 || N == 0) return ok();
+  if (!offsets_dev || !aligned(offsets_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned offsets", name);
+  if (!aligned(a_s_dev, 4) || !aligned(w_s_dev, 4)) return fail(VDTQ_EINVAL, "%s: scales need 4 bytes alignment", name);
+  if (K % 128) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is not a multiple of 128", name, (long long)K);
+  hipError_t e = vdtq::launch_qgemm_mx_grouped(a_fmt == VDTQ_FMT_MXFP8, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev,
+                                               offsets_dev, E, y_dev, ldy, out_dtype, T, N, K,
+                                               static_cast<hipStream_t>(stream));
+  return hip_status(e, "qgemm_mx_grouped launch");
+}
+
 int block_stats(const void* in_dev, const void* out_dev, const void* dprev_dev, void* dnew_dev, int64_t n,
                 double* stats_dev, void* ws_dev, size_t ws_bytes, void* stream) {
   if (n < 0) return fail(VDTQ_EINVAL, "block_stats: n=%lld < 0", (long long)n);

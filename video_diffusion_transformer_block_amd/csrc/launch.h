@@ -56,6 +56,20 @@ hipError_t launch_qgemm_mx_quant(bool a_fp8, const uint8_t* a_q, const uint8_t* 
                                  const uint8_t* w_s, const float* bias, bool out_fp8, bool gelu, uint8_t* q_out,
                                  uint8_t* s_out, int64_t M, int64_t N, int64_t K, hipStream_t st);
 
+hipError_t launch_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* res, int64_t ldr,
+                                   const float* gain, float eps, int b, int fmt, void* sum, int64_t lds, void* q,
+                                   void* scales, hipStream_t st);
+
+// act: 0 bf16, 1 INT8 (both with NVFP4 weights), 2 MXFP8, 3 MXFP4 (both with
+// MXFP4 weights)
+hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t* w_q, const uint8_t* w_s,
+                        const float* w_ts, const float* bias, void* y, int64_t ldy, int out_dtype, int64_t M,
+                        int64_t N, int64_t K, hipStream_t st);
+
+hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
+                                   const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E, void* y,
+                                   int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, hipStream_t st);
+
 size_t bs_workspace_bytes(int64_t n);
 hipError_t launch_block_stats(const void* in, const void* out, const void* dprev, void* dnew,
                               int64_t n, double* stats, void* ws, hipStream_t st);

@@ -3,6 +3,7 @@ marshalling only.  torch provides device memory and the current HIP stream;
 every step of the computation runs in libvdtq.so."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -19,6 +20,14 @@ def _p(t: Optional[torch.Tensor]):
 
 def _stream(dev: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _on(dev: torch.device):
+    """Makes dev the current device around a launch: a launch needs its
+    stream's device to be the current one."""
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
 
 
 # Device type every tensor handed to the library must have (the CPU tests of
@@ -262,6 +271,11 @@ def _out(M, N, out_dtype, dev, y):
     return y
 
 
+def _ldy(y: torch.Tensor) -> int:
+    """Row stride of an output; a single row's may be anything."""
+    return max(y.stride(0), y.shape[1]) if y.shape[0] > 1 else y.shape[1]
+
+
 def qgemm_w4a4(a: NVFP4Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
                out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
     M, K = a.q.shape[0], a.q.shape[1] * 2
@@ -365,6 +379,170 @@ def qgemm_mx_quant(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None
                                    L.FMT_MXFP4 if out_fmt == "mxfp4" else L.FMT_MXFP8, L.GELU if gelu else 0,
                                    _p(out.q), _p(out.scales), M, N, K, _stream(dev)))
     return out
+
+
+def _rows(t: torch.Tensor, name: str, M: int, K: int, dev: torch.device):
+    """A bf16 [M, K] tensor on dev with unit column stride (its row stride is
+    passed on)."""
+    _require(t, torch.bfloat16, name)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != (M, K) or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{M}, {K}] with unit column stride, got shape {tuple(t.shape)} "
+                         f"strides {tuple(t.stride())}")
+    return t
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride in elements; the stride of a single row means nothing."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     residual: Optional[torch.Tensor] = None, eps: float = 1e-6, had_block: int = 64,
+                     fmt: str = "int8", out=None, sum_out: Optional[torch.Tensor] = None):
+    """Residual addition, RMS norm, block Hadamard transform and INT8, BF16,
+    MXFP4 or MXFP8 quantization of bf16 rows in one pass.  weight: fp32 [K]
+    or None.  Returns (quantized tensor, residual stream): the stream is
+    bf16(x + residual), written to sum_out when given (x or residual itself
+    updates it in place), or None without a residual.  out: a previously
+    returned tensor of the same format and shape whose buffers are reused."""
+    _require(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    M, K = x.shape
+    dev = x.device
+    _rows(x, "x", M, K, dev)
+    if fmt not in ("int8", "bf16", "mxfp4", "mxfp8"):
+        raise ValueError(f"fmt {fmt!r}")
+    if K % 16 or (fmt in ("mxfp4", "mxfp8") and K % 32):
+        raise ValueError(f"K = {K} is not a multiple of {32 if fmt in ('mxfp4', 'mxfp8') else 16}")
+    if weight is not None:
+        _buf(weight, "weight", torch.float32, (K,), dev)
+    ldr = lds = 0
+    if residual is not None:
+        ldr = _row_stride(_rows(residual, "residual", M, K, dev))
+        if sum_out is None:
+            sum_out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        lds = _row_stride(_rows(sum_out, "sum_out", M, K, dev))
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if fmt == "int8":
+        if out is None:
+            out = INT8Tensor(torch.empty((M, K), dtype=torch.int8, device=dev),
+                             torch.empty((M,), dtype=torch.float32, device=dev))
+        else:
+            _buf(out.q, "out.q", torch.int8, (M, K), dev)
+            _buf(out.scales, "out.scales", torch.float32, (M,), dev)
+        fcode, s = L.FMT_INT8, out.scales
+    elif fmt == "bf16":
+        if out is None:
+            out = BF16Tensor(torch.empty((M, K), dtype=torch.bfloat16, device=dev))
+        else:
+            _buf(out.q, "out.q", torch.bfloat16, (M, K), dev)
+        fcode, s = L.FMT_BF16, None
+    else:
+        if out is None:
+            out = MXTensor(torch.empty((M, K // 2 if fmt == "mxfp4" else K), dtype=torch.uint8, device=dev),
+                           torch.empty((M, K // 32), dtype=torch.uint8, device=dev), fmt)
+        elif out.fmt != fmt:
+            raise ValueError(f"out holds {out.fmt}, asked for {fmt}")
+        else:
+            _mx(out, "out", M, K, dev)
+        fcode, s = L.FMT_MXFP4 if fmt == "mxfp4" else L.FMT_MXFP8, out.scales
+    with _on(dev):
+        L.check(L.lib().rmsnorm_quantize(_p(x), M, K, _row_stride(x), _p(residual), ldr, _p(weight), eps, had_block,
+                                         fcode, _p(sum_out), lds, _p(out.q), _p(s), _stream(dev)))
+    return out, sum_out
+
+
+def qgemv_w4a16(a: BF16Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
+                out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qgemm_w4a16 for at most 32 rows."""
+    _require(a.q, torch.bfloat16, "a.q")
+    if a.q.dim() != 2 or not a.q.is_contiguous():
+        raise ValueError("a.q must be a contiguous [M, K] tensor")
+    M, K = a.q.shape
+    N = w.q.shape[0]
+    dev = a.q.device
+    _nvfp4(w, "w", N, K, dev)
+    _bias(bias, N, dev)
+    y = _out(M, N, out_dtype, dev, y)
+    with _on(dev):
+        L.check(L.lib().qgemv_w4a16(_p(a.q), _p(w.q), _p(w.scales), _p(w.ts), _p(bias), _p(y), _ldy(y),
+                                    L.OUT_BF16 if out_dtype == "bf16" else L.OUT_F32, M, N, K, _stream(dev)))
+    return y
+
+
+def qgemv_w4a8(a: INT8Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
+               out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qgemm_w4a8 for at most 32 rows."""
+    M, K = a.q.shape
+    N = w.q.shape[0]
+    dev = a.q.device
+    _buf(a.q, "a.q", torch.int8, (M, K), dev)
+    _buf(a.scales, "a.scales", torch.float32, (M,), dev)
+    _nvfp4(w, "w", N, K, dev)
+    _bias(bias, N, dev)
+    y = _out(M, N, out_dtype, dev, y)
+    with _on(dev):
+        L.check(L.lib().qgemv_w4a8(_p(a.q), _p(a.scales), _p(w.q), _p(w.scales), _p(w.ts), _p(bias), _p(y), _ldy(y),
+                                   L.OUT_BF16 if out_dtype == "bf16" else L.OUT_F32, M, N, K, _stream(dev)))
+    return y
+
+
+def qgemv_mx(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None,
+             out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qgemm_mx for at most 32 rows, with every product exact and added in
+    fp32."""
+    if w.fmt != "mxfp4":
+        raise ValueError("MX weights must be mxfp4")
+    M = a.q.shape[0]
+    K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
+    N = w.q.shape[0]
+    dev = a.q.device
+    _mx(a, "a", M, K, dev)
+    _mx(w, "w", N, K, dev)
+    _bias(bias, N, dev)
+    y = _out(M, N, out_dtype, dev, y)
+    with _on(dev):
+        L.check(L.lib().qgemv_mx(L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, _p(a.q), _p(a.scales), _p(w.q),
+                                 _p(w.scales), _p(bias), _p(y), _ldy(y),
+                                 L.OUT_BF16 if out_dtype == "bf16" else L.OUT_F32, M, N, K, _stream(dev)))
+    return y
+
+
+def qgemm_mx_grouped(a: MXTensor, w: MXTensor, offsets: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """MX product with weights per group of rows: rows offsets[e] ..
+    offsets[e+1] - 1 of a times the weights of expert e.  w holds the experts'
+    [N, K] weights stacked to [E * N, K] rows (hadamard_quantize of the
+    stacked weights), offsets is an int32 device tensor [E + 1], bias fp32
+    [E, N].  Rows outside offsets[0] .. offsets[E] of y stay as they were
+    (uninitialised in a new y)."""
+    if w.fmt != "mxfp4":
+        raise ValueError("MX weights must be mxfp4")
+    T = a.q.shape[0]
+    K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
+    dev = a.q.device
+    _mx(a, "a", T, K, dev)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError(f"offsets must be a 1-D tensor of E + 1 values, got shape {tuple(offsets.shape)}")
+    E = offsets.numel() - 1
+    _buf(offsets, "offsets", torch.int32, (E + 1,), dev)
+    rows = w.q.shape[0]
+    if rows % E if E else rows:
+        raise ValueError(f"w has {rows} rows, not a multiple of the {E} experts")
+    N = rows // E if E else 0
+    _mx(w, "w", rows, K, dev)
+    if bias is not None:
+        _buf(bias, "bias", torch.float32, (E, N), dev)
+    y = _out(T, N, out_dtype, dev, y)
+    with _on(dev):
+        L.check(L.lib().qgemm_mx_grouped(L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, _p(a.q), _p(a.scales),
+                                         _p(w.q), _p(w.scales), _p(bias), _p(offsets), E, _p(y), _ldy(y),
+                                         L.OUT_BF16 if out_dtype == "bf16" else L.OUT_F32, T, N, K, _stream(dev)))
+    return y
 
 
 def block_stats(inp: torch.Tensor, out: torch.Tensor, dprev: Optional[torch.Tensor] = None,
