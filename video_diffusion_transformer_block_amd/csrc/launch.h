@@ -66,6 +66,17 @@ hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t
                         const float* w_ts, const float* bias, void* y, int64_t ldy, int out_dtype, int64_t M,
                         int64_t N, int64_t K, hipStream_t st);
 
+// Lets a kernel use `bytes` of dynamic LDS on the current device.
+inline hipError_t allow_lds(const void* kernel, int bytes) {
+  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Rows grouped by expert: tiles of 256 x 256 (qgemm_mx.hip), and the choice
+// between them and the few-row kernel.
+hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
+                                       const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E,
+                                       void* y, int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K,
+                                       hipStream_t st);
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
                                    const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E, void* y,
                                    int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, hipStream_t st);

@@ -41,6 +41,9 @@ struct GemmParams {
   uint8_t* s_out;          // [M][N / 32] E8M0 scales
   uint32_t qflags;         // 4: GELU before the transform
   const uint16_t* gtab;    // the device's GELU table (qflags 4)
+  // rows grouped by expert: M is the number of rows, offsets holds E + 1
+  const int32_t* offsets;
+  int32_t experts;
 };
 
 // Partial tile of slice `sl` of split tile `tile`.  Layout inside a slot:

@@ -56,6 +56,7 @@
 #include "launch.h"
 #include "lds_dma.h"
 #include "qgemm_common.h"
+#include "row_groups.h"
 
 namespace vdtq {
 
@@ -182,7 +183,10 @@ __device__ __forceinline__ void quant_store_tile(const GemmParams& p, const floa
 // otherwise per-element stores.  QOUT 1 / 2: the quantizing epilogue with
 // MXFP4 / MXFP8 codes (the GELU table sits after the ring).  One epilogue
 // per instantiation keeps the accumulators in AGPRs until they are read.
-template <bool A8, bool QUADS, bool SPLIT, bool STAGED, int QOUT = 0>
+// GROUPED: the tile's rows belong to one expert and are multiplied with that
+// expert's weights (row_groups.h); the pointers move to its first row and
+// weights, and M becomes the expert's rows from there on.
+template <bool A8, bool QUADS, bool SPLIT, bool STAGED, int QOUT = 0, bool GROUPED = false>
 __global__ __launch_bounds__(GT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void qgemm_mx_kernel(GemmParams p) {
   using P = MxPipe<A8, QUADS>;
@@ -200,6 +204,13 @@ void qgemm_mx_kernel(GemmParams p) {
     const int sl = (int)(blockIdx.x / p.sk_tiles);
     kb = sl * p.slice_nk;
     ke = min(p.nk, kb + p.slice_nk);
+  } else if constexpr (GROUPED) {
+    p.tiles_m = row_tiles(p.offsets, p.experts, p.M, 256);
+    const int tiles = p.tiles_m * p.tiles_n;
+    if ((int)blockIdx.x >= tiles) return;            // the grid is an upper bound
+    tile = xcd_range_id(blockIdx.x, tiles);
+    kb = 0;
+    ke = p.nk;
   } else {
     tile = p.sk_tiles + xcd_range_id(blockIdx.x, gridDim.x);
     kb = 0;
@@ -207,6 +218,17 @@ void qgemm_mx_kernel(GemmParams p) {
   }
   int tm, tn;
   tile_coords(tile, p.tiles_m, p.tiles_n, tm, tn);
+  if constexpr (GROUPED) {
+    const RowTile g = row_tile(p.offsets, p.experts, p.M, 256, tm);
+    p.M = g.rows;
+    p.a_q = static_cast<const uint8_t*>(p.a_q) + (int64_t)g.row0 * (A8 ? K : K / 2);
+    p.a_s = static_cast<const uint8_t*>(p.a_s) + (int64_t)g.row0 * (K / 32);
+    p.w_q += (int64_t)g.expert * p.N * (K / 2);
+    p.w_s += (int64_t)g.expert * p.N * (K / 32);
+    if (p.bias) p.bias += (int64_t)g.expert * p.N;
+    p.y = static_cast<uint8_t*>(p.y) + (int64_t)g.row0 * p.ldy * (p.out_f32 ? 4 : 2);
+    tm = 0;
+  }
   const int m0 = tm * 256, n0 = tn * 256;
 
   const uint8_t* aq = static_cast<const uint8_t*>(p.a_q);
@@ -432,6 +454,16 @@ static size_t mx_lds_bytes() {
   return QOUT ? (size_t)MxPipe<A8, QUADS>::GTAB + kGeluTabBytes : (size_t)MxPipe<A8, QUADS>::LDS;
 }
 
+template <bool A8, bool QUADS, bool STAGED>
+static hipError_t launch_mx_grouped(const GemmParams& p, unsigned grid, hipStream_t st) {
+  const auto kernel = &qgemm_mx_kernel<A8, QUADS, false, STAGED, 0, true>;
+  const int lds = MxPipe<A8, QUADS>::LDS;
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((qgemm_mx_kernel<A8, QUADS, false, STAGED, 0, true>), dim3(grid), dim3(GT), lds, st, p);
+  return hipGetLastError();
+}
+
 template <bool A8, bool QUADS, bool SPLIT, bool STAGED, int QOUT = 0>
 static hipError_t set_mx_lds_attr() {
   static bool attr_set = false;
@@ -513,6 +545,32 @@ hipError_t launch_qgemm_mx_quant(bool a_fp8, const uint8_t* a_q, const uint8_t* 
   }
   if (a_fp8) return out_fp8 ? launch_mx_quant<true, false, 2>(p, st) : launch_mx_quant<true, false, 1>(p, st);
   return out_fp8 ? launch_mx_quant<false, false, 2>(p, st) : launch_mx_quant<false, false, 1>(p, st);
+}
+
+hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
+                                       const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E,
+                                       void* y, int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K,
+                                       hipStream_t st) {
+  GemmParams p{};
+  p.a_q = a_q; p.a_s = a_s;
+  p.w_q = w_q; p.w_s = w_s;
+  p.bias = bias; p.y = y; p.ldy = ldy;
+  p.M = (int32_t)T; p.N = (int32_t)N; p.K = (int32_t)K;
+  p.out_f32 = out_dtype == 1;
+  p.tiles_n = (p.N + 255) / 256;
+  p.nk = p.K / BK;
+  p.offsets = offsets;
+  p.experts = (int32_t)E;
+  const unsigned grid = (unsigned)((T / 256 + E) * p.tiles_n);
+  // the device-side staged_store_ok, for every expert's bias and rows
+  const bool staged = !p.out_f32 && (p.N % 8) == 0 && (p.ldy % 8) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 &&
+                      (!p.bias || (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0);
+  if (mx_quads(K)) {
+    if (a_fp8) return staged ? launch_mx_grouped<true, true, true>(p, grid, st) : launch_mx_grouped<true, true, false>(p, grid, st);
+    return staged ? launch_mx_grouped<false, true, true>(p, grid, st) : launch_mx_grouped<false, true, false>(p, grid, st);
+  }
+  if (a_fp8) return staged ? launch_mx_grouped<true, false, true>(p, grid, st) : launch_mx_grouped<true, false, false>(p, grid, st);
+  return staged ? launch_mx_grouped<false, false, true>(p, grid, st) : launch_mx_grouped<false, false, false>(p, grid, st);
 }
 
 hipError_t launch_qgemm_mx(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,

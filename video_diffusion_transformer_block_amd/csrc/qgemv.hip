@@ -14,6 +14,7 @@
 #include "device_common.h"
 #include "launch.h"
 #include "lds_dma.h"
+#include "row_groups.h"
 
 namespace vdtq {
 
@@ -98,25 +99,11 @@ __global__ __launch_bounds__(512) void qgemv_kernel(GemvParams p) {
   const int n0 = blockIdx.x * 16;
   int64_t m0 = 0, rows = p.M, expert = 0;
   if (p.offsets) {
-    // the block of rows: experts in order, each in blocks of 16 MT rows.
-    // An offset is taken as the largest up to there, inside [0, M], so that
-    // no bad offset reaches past the rows or gives a row to two experts
-    int64_t blk = blockIdx.y;
-    int lo = min(max(p.offsets[0], 0), p.M);
-    rows = 0;
-    for (int e = 0; e < p.E; ++e) {
-      const int hi = max(lo, min(p.offsets[e + 1], p.M));
-      const int64_t nb = (hi - lo + 16 * MT - 1) / (16 * MT);
-      if (blk < nb) {
-        m0 = lo + blk * 16 * MT;
-        rows = hi;
-        expert = e;
-        break;
-      }
-      blk -= nb;
-      lo = hi;
-    }
-    if (rows == 0) return;
+    const RowTile t = row_tile(p.offsets, p.E, p.M, 16 * MT, blockIdx.y);
+    if (t.rows <= 0) return;                          // the grid is an upper bound
+    m0 = t.row0;
+    rows = m0 + t.rows;
+    expert = t.expert;
   }
   const uint8_t* wq = p.w_q + expert * p.N * (int64_t)(p.K / 2);
   const uint8_t* wsc = p.w_s + expert * p.N * (int64_t)(p.K / (MX ? 32 : 16));
@@ -209,6 +196,8 @@ hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t
                                    const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E, void* y,
                                    int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, hipStream_t st) {
   if (T == 0 || N == 0) return hipSuccess;
+  if (T / E >= 64 && (out_dtype == 0 || !a_fp8))
+    return launch_qgemm_mx_grouped_256(a_fp8, a_q, a_s, w_q, w_s, bias, offsets, E, y, ldy, out_dtype, T, N, K, st);
   GemvParams p{};
   p.a_q = a_q; p.a_s = a_s;
   p.w_q = w_q; p.w_s = w_s; p.bias = bias; p.offsets = offsets;
