@@ -426,7 +426,8 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * No workspace.  A NaN in an activation row, in its scale (INT8) or an
  * 0xFF scale byte (MX) makes that row of Y NaN and no other.
  * Errors: VDTQ_EINVAL for null or misaligned pointers, bad sizes or
- * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS.
+ * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS or
+ * K > 2^25.
  */
 #define VDTQ_GEMV_MAX_ROWS 32
 int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev,
@@ -468,7 +469,7 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  * K              > 0, multiple of 32
  * No workspace.
  * Errors: VDTQ_EINVAL for a bad a_fmt or size, null or misaligned pointers,
- * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128.
+ * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128 or K > 2^25.
  */
 int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
                      const uint8_t* w_q_dev, const uint8_t* w_s_dev,

@@ -67,6 +67,7 @@ def _gemv(fn, **kw):
     (dict(od=2), L.EINVAL), (dict(aq=None), L.EINVAL), (dict(wq=None), L.EINVAL), (dict(ws=None), L.EINVAL),
     (dict(y=None), L.EINVAL), (dict(aq=ODD), L.EINVAL), (dict(wq=ODD), L.EINVAL), (dict(M=33), L.EUNSUPPORTED),
     (dict(bias=ctypes.c_void_p(0x100002)), L.EINVAL), (dict(M=1 << 31), L.EINVAL),
+    (dict(K=(1 << 25) + 128), L.EUNSUPPORTED),
 ])
 def test_qgemv_rejects(fn, kw, code):
     assert _gemv(fn, **kw) == code
@@ -92,7 +93,7 @@ def _grp(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(fmt=L.FMT_NVFP4), L.EINVAL), (dict(E=-1), L.EINVAL), (dict(E=65537), L.EINVAL), (dict(K=0), L.EINVAL),
-    (dict(K=48), L.EINVAL), (dict(K=96), L.EUNSUPPORTED), (dict(T=-1), L.EINVAL), (dict(N=-1), L.EINVAL),
+    (dict(K=48), L.EINVAL), (dict(K=96), L.EUNSUPPORTED), (dict(K=(1 << 25) + 128), L.EUNSUPPORTED), (dict(T=-1), L.EINVAL), (dict(N=-1), L.EINVAL),
     (dict(ldy=10), L.EINVAL), (dict(od=3), L.EINVAL), (dict(off=None), L.EINVAL), (dict(aq=None), L.EINVAL),
     (dict(as_=None), L.EINVAL), (dict(wq=None), L.EINVAL), (dict(ws=None), L.EINVAL), (dict(y=None), L.EINVAL),
     (dict(aq=ODD), L.EINVAL), (dict(off=ctypes.c_void_p(0x100002)), L.EINVAL),

@@ -330,7 +330,7 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
                        const float* bias, const void* y, int64_t ldy, int out_dtype, int64_t M, int64_t N, int64_t K,
                        int kmul) {
   if (M < 0 || M > kI32 || N < 0 || N > kI32) return fail(VDTQ_EINVAL, "%s: M=%lld N=%lld out of range", name, (long long)M, (long long)N);
-  if (K <= 0 || K > kI32 - 4096 || K % kmul)
+  if (K <= 0 || K > kI32 || K % kmul)
     return fail(VDTQ_EINVAL, "%s: K=%lld must be a positive multiple of %d", name, (long long)K, kmul);
   if (out_dtype != VDTQ_OUT_BF16 && out_dtype != VDTQ_OUT_F32) return fail(VDTQ_EINVAL, "%s: out_dtype=%d", name, out_dtype);
   if (ldy < N) return fail(VDTQ_EINVAL, "%s: ldy=%lld < N=%lld", name, (long long)ldy, (long long)N);
@@ -338,6 +338,7 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
   if (!a_q || !a_s || !w_q || !w_s || !y) return fail(VDTQ_EINVAL, "%s: null pointer argument", name);
   if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(y, out_dtype ? 4 : 2) || (bias && !aligned(bias, 4)))
     return fail(VDTQ_EINVAL, "%s: misaligned pointer (codes need 16 bytes)", name);
+  if (K > (1 << 25)) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is above 2^25", name, (long long)K);
   return VDTQ_OK;
 }
 

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace vdtq {
 
 // Compute units of the current device, cached per device; `fallback` when
@@ -69,6 +71,21 @@ hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t
 // Lets a kernel use `bytes` of dynamic LDS on the current device.
 inline hipError_t allow_lds(const void* kernel, int bytes) {
   return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// allow_lds once per device and kernel (ID tells a file's kernels apart): the
+// call takes as long as a launch.  Two threads may both do it, with the same
+// effect.
+template <int ID>
+static hipError_t allow_lds_once(const void* kernel, int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return hipSuccess;
+  e = allow_lds(kernel, bytes);
+  if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // Rows grouped by expert: tiles of 256 x 256 (qgemm_mx.hip), and the choice

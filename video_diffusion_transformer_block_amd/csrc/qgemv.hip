@@ -4,13 +4,35 @@
 //
 // The mathematics: W[n][k] = e2m1(code) * scale(n, k / G) with an E4M3 scale
 // per G = 16 elements (NVFP4, and one fp32 tensor scale) or an E8M0 scale per
-// G = 32 (MXFP4).  Every A and W element is exact in bf16 (E2M1 x E4M3 has at
-// most 6 significant bits, INT8 7, E4M3 4; E8M0 is a power of two), so the
-// products are exact and v_mfma_f32_16x16x32_bf16 adds them in fp32.  The
-// block-scaled matrix instruction is not used here: with E4M3 operands it
-// drops low bits of the products (3.4e-5 relative error of the sum, measured
-// over K = 128 .. 12288), and with so few rows the matrix cores are idle
-// most of the time anyway.
+// G = 32 (MXFP4).  Operands are decoded exactly and multiplied by
+// v_mfma_f32_16x16x32, whose products are exact and whose sums are fp32:
+//   bf16 and MX activations: in bf16 (E2M1 x E4M3 has at most 6 significant
+//     bits, E4M3 4, E8M0 is a power of two that the conversion applies);
+//   INT8 activations: in fp16 (7 bits; E2M1 x E4M3 is 2^-10 .. 2688), whose
+//     packed multiply decodes NVFP4 in half the instructions.
+// The block-scaled matrix instruction is not used here: with E4M3 operands it
+// cuts small products against the largest of eight (3.4e-5 relative error of
+// the sum, measured over K = 128 .. 12288), and with so few rows the matrix
+// cores are idle most of the time anyway.
+//
+// Split: a workgroup owns 16 features (and up to 32 rows), its wavefronts
+// take steps of K in turn; the sums meet in LDS in wavefront order.  K is not
+// split over workgroups: 16 features a workgroup already fill the card from
+// N = 4096 on, and a second launch or a counter would cost more than the idle
+// units of a smaller N.
+//
+// Loads: lane l of the matrix instruction holds feature (or row) l % 16, so
+// fragments read straight from memory touch 64 places of 16 bytes each, and a
+// compute unit looks up about one place a cycle (such a kernel took 18 us for
+// 32 rows, K = 1920, N = 7679, against 8 here).  Instead a wavefront reads whole runs of rows
+// (1 KB an instruction), puts them into LDS of its own (no barrier: its LDS
+// operations run in order) and takes the fragments from there; the next
+// step's loads are in flight meanwhile.  Rows of 16-byte pieces are stored
+// with piece p of row r at p ^ (r & 7), which spreads the eight rows that a
+// fragment read takes at a time over all banks.  The loads go through buffer
+// resources: rows past M or N and elements past K read as zeros.
+#include <algorithm>
+
 #include "device_common.h"
 #include "launch.h"
 #include "lds_dma.h"
@@ -19,6 +41,7 @@
 namespace vdtq {
 
 typedef __bf16 gv_bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 gv_bf16x2 __attribute__((ext_vector_type(2)));
 
 // activation formats
 constexpr int kActBf16 = 0, kActInt8 = 1, kActMx8 = 2, kActMx4 = 3;
@@ -35,144 +58,341 @@ struct GemvParams {
   int64_t ldy;
   int32_t M, N, K, E;
   int32_t out_f32;
+  int32_t tiles;             // feature tiles of a workgroup
 };
 
-// 8 bf16 of packed E2M1 codes (one dword) times a scale
-__device__ __forceinline__ gv_bf16x8 decode_w8(uint32_t c, float sc) {
-  gv_bf16x8 o;
-  float2v f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
-  o[0] = (__bf16)(f[0] * sc); o[1] = (__bf16)(f[1] * sc);
-  f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-  o[2] = (__bf16)(f[0] * sc); o[3] = (__bf16)(f[1] * sc);
-  f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
-  o[4] = (__bf16)(f[0] * sc); o[5] = (__bf16)(f[1] * sc);
-  f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
-  o[6] = (__bf16)(f[0] * sc); o[7] = (__bf16)(f[1] * sc);
+// One operand of the matrix instruction, 8 values: fp16 for INT8
+// activations, bf16 otherwise.
+template <int AF>
+struct GvFrag {
+  uint32_t w[4];
+};
+
+template <int AF>
+__device__ __forceinline__ float4v gv_mfma(const GvFrag<AF>& a, const GvFrag<AF>& b, float4v c) {
+  const uint4 x = make_uint4(a.w[0], a.w[1], a.w[2], a.w[3]), y = make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
+  if constexpr (AF == kActInt8)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, x), __builtin_bit_cast(half8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(gv_bf16x8, x), __builtin_bit_cast(gv_bf16x8, y), c, 0, 0, 0);
+}
+
+// E8M0 byte as the scale operand of the conversions, which read its exponent
+// field: 2^(b - 127)
+__device__ __forceinline__ float e8m0(uint32_t b) { return __uint_as_float(b << 23); }
+
+// 8 packed E2M1 codes (one dword) times the E8M0 scale, bf16
+template <int AF>
+__device__ __forceinline__ GvFrag<AF> decode_mx4(uint32_t c, float sc) {
+  GvFrag<AF> o;
+  o.w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 0));
+  o.w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 1));
+  o.w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 2));
+  o.w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 3));
   return o;
 }
 
-// E8M0 byte as fp32: 2^(b - 127), NaN for 255 (byte 0 is the subnormal 2^-127)
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return b == 0xFFu ? __builtin_nanf("") : b ? __uint_as_float(b << 23) : 0x1p-127f;
+// 8 packed E2M1 codes times the E4M3 scale byte (exact): fp16 by a packed
+// multiplication, bf16 by way of fp32 (there is no packed bf16 multiply)
+template <int AF>
+__device__ __forceinline__ GvFrag<AF> decode_nv(uint32_t c, float sc) {
+  GvFrag<AF> o;
+  if constexpr (AF == kActInt8) {
+    const half2v s = {(_Float16)sc, (_Float16)sc};
+    o.w[0] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 0) * s));
+    o.w[1] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * s));
+    o.w[2] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * s));
+    o.w[3] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * s));
+  } else {
+    auto pair = [&](float2v f) {
+      const gv_bf16x2 v = {(__bf16)(f[0] * sc), (__bf16)(f[1] * sc)};
+      return __builtin_bit_cast(uint32_t, v);
+    };
+    o.w[0] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0));
+    o.w[1] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1));
+    o.w[2] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2));
+    o.w[3] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3));
+  }
+  return o;
 }
 
-// The 8 activations of row m at k .. k + 7 as bf16 (zeros past M or K).
+// 8 INT8 codes (two dwords) as fp16: the byte with its sign bit flipped is
+// q + 128, under the exponent of 1024 it reads 1024 + q + 128
+__device__ __forceinline__ void decode_i8(uint32_t lo, uint32_t hi, uint32_t (&o)[4]) {
+  const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const uint32_t x = lo ^ 0x80808080u, y = hi ^ 0x80808080u;
+  o[0] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) - off));
+  o[1] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) - off));
+  o[2] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, y, 0x04010400u)) - off));
+  o[3] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, y, 0x04030402u)) - off));
+}
+
+// bytes of 32 activations, and the 16-byte loads they take
 template <int AF>
-__device__ __forceinline__ gv_bf16x8 load_a8(const GemvParams& p, int64_t m, bool live, int k) {
-  gv_bf16x8 o = __builtin_bit_cast(gv_bf16x8, make_uint4(0u, 0u, 0u, 0u));
-  if (!live || k >= p.K) return o;
+struct ActBytes {
+  static constexpr int n = AF == kActBf16 ? 64 : AF == kActMx4 ? 16 : 32;
+  static constexpr int loads = n / 16;
+};
+
+// activations 8 j .. 8 j + 7 of the 32 in w
+template <int AF>
+__device__ __forceinline__ GvFrag<AF> decode_act(const uint4 (&w)[ActBytes<AF>::loads], float sc, int j) {
+  GvFrag<AF> o;
   if constexpr (AF == kActBf16) {
-    o = __builtin_bit_cast(gv_bf16x8, *reinterpret_cast<const uint4*>(p.a_q + 2 * (m * p.K + k)));
-  } else if constexpr (AF == kActInt8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p.a_q + m * p.K + k);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[e] = (__bf16)(float)(int8_t)(w.x >> (8 * e));
-      o[4 + e] = (__bf16)(float)(int8_t)(w.y >> (8 * e));
-    }
+    o.w[0] = w[j].x; o.w[1] = w[j].y; o.w[2] = w[j].z; o.w[3] = w[j].w;
+  } else if constexpr (AF == kActMx4) {
+    o = decode_mx4<AF>(j == 0 ? w[0].x : j == 1 ? w[0].y : j == 2 ? w[0].z : w[0].w, sc);
   } else {
-    const float sc = e8m0(static_cast<const uint8_t*>(p.a_s)[m * (p.K / 32) + k / 32]);
-    if constexpr (AF == kActMx8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p.a_q + m * p.K + k);
-      o[0] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.x, 0) * sc); o[1] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.x, 1) * sc);
-      o[2] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.x, 2) * sc); o[3] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.x, 3) * sc);
-      o[4] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.y, 0) * sc); o[5] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.y, 1) * sc);
-      o[6] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.y, 2) * sc); o[7] = (__bf16)(__builtin_amdgcn_cvt_f32_fp8(w.y, 3) * sc);
+    const uint4 v = w[j >> 1];
+    const uint32_t lo = j & 1 ? v.z : v.x, hi = j & 1 ? v.w : v.y;
+    if constexpr (AF == kActInt8) {
+      decode_i8(lo, hi, o.w);
     } else {
-      o = decode_w8(*reinterpret_cast<const uint32_t*>(p.a_q + m * (p.K / 2) + k / 2), sc);
+      o.w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, false));
+      o.w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, true));
+      o.w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, sc, false));
+      o.w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, sc, true));
     }
   }
   return o;
 }
 
-// One workgroup: 16 features x up to 32 rows (MT tiles of 16), the wavefronts
-// taking 128-element steps of K in turn and their sums joined through LDS in
-// wavefront order.  Operand layout: lane l holds row / feature l % 16, its
-// 32 codes of a step k = 32 (l / 16) .. +31 feed four instructions of 8 each.
-template <int AF, int MT>
-__global__ __launch_bounds__(512) void qgemv_kernel(GemvParams p) {
-  constexpr bool MX = AF >= kActMx8;
-  constexpr int NW = 8;
-  __shared__ float part[NW][MT * 16][16];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+constexpr int kGvMaxLds = 160 * 1024;
+constexpr uint32_t kGvNone = 0xFFFFFFF0u;    // an offset past every buffer: reads zeros
+typedef uint32_t gv_uint2 __attribute__((ext_vector_type(2)));
+
+// The shape of a wavefront's step for an activation format and up to MR rows
+// (4, 16 or 32).
+template <int AF, int MR>
+struct GvStep {
+  static constexpr bool MX = AF >= kActMx8;
+  static constexpr int MT = (MR + 15) / 16;     // tiles of 16 rows
+  static constexpr int KS = (AF == kActBf16 || MR == 32) ? 256 : 512;  // K
+  static constexpr int WAVES = MR == 32 ? 8 : 16;                      // at most
+  static constexpr int U = KS / 128;            // 32-element pieces a lane takes
+  static constexpr int WROW = KS / 2;           // code bytes of a feature
+  static constexpr int WLOADS = 16 * WROW / 1024;
+  static constexpr int AROW = KS * ActBytes<AF>::n / 32;
+  static constexpr int ALOADS = (MR * AROW + 1023) / 1024;
+  static constexpr int ALOAD_ROWS = 1024 / AROW;
+  static constexpr int LDS = 16 * WROW + ALOADS * 1024;                // bytes of a wavefront
+  static constexpr int SB = KS / 4 / (MX ? 32 : 16);   // scale bytes of a lane
+};
+
+// The SB scale bytes at `off` (of the elements from k on), low byte first.
+template <int SB, int G>
+__device__ __forceinline__ gv_uint2 load_scales(__amdgpu_buffer_rsrc_t rs, uint32_t off, int k, int K) {
+  gv_uint2 d = {0u, 0u};
+  if (K % 128 == 0) {                           // runs of SB bytes, aligned, whole
+    const uint32_t o = k < K ? off : kGvNone;
+    if constexpr (SB == 8) d = __builtin_amdgcn_raw_buffer_load_b64(rs, o, 0, 0);
+    else if constexpr (SB == 4) d[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
+    else d[0] = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+  } else {
+#pragma unroll
+    for (int b = 0; b < SB; ++b)
+      d[b >> 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, k + G * b < K ? off + b : kGvNone, 0, 0) << (8 * (b & 3));
+  }
+  return d;
+}
+
+template <int AF, int MR>
+__global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams p) {
+  using S = GvStep<AF, MR>;
+  constexpr int MT = S::MT;
+  constexpr bool MX = S::MX;
+  constexpr int G = MX ? 32 : 16, KS = S::KS, U = S::U;
+  extern __shared__ __attribute__((aligned(16))) uint8_t gv_lds[];
+  const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  int64_t m0 = 0, rows = p.M, expert = 0;
+  const int K = p.K;
+  int64_t m0 = 0, expert = 0;
+  int rows = p.M;
   if (p.offsets) {
-    const RowTile t = row_tile(p.offsets, p.E, p.M, 16 * MT, blockIdx.y);
-    if (t.rows <= 0) return;                          // the grid is an upper bound
+    const RowTile t = row_tile(p.offsets, p.E, p.M, MR, blockIdx.y);
+    if (t.rows <= 0) return;                    // the grid is an upper bound
     m0 = t.row0;
-    rows = m0 + t.rows;
+    rows = min(t.rows, MR);
     expert = t.expert;
   }
-  const uint8_t* wq = p.w_q + expert * p.N * (int64_t)(p.K / 2);
-  const uint8_t* wsc = p.w_s + expert * p.N * (int64_t)(p.K / (MX ? 32 : 16));
-  const int64_t n = min(n0 + r, p.N - 1);          // features past N repeat the last, never stored
+  const uint32_t arow = AF == kActBf16 ? 2u * K : AF == kActMx4 ? K / 2u : (uint32_t)K;
+  const uint32_t wrow = K / 2, srow = K / G;
+  const __amdgpu_buffer_rsrc_t aq = raw_buffer(p.a_q + m0 * arow, rows * arow);
+  const __amdgpu_buffer_rsrc_t as =
+      raw_buffer(MX ? static_cast<const uint8_t*>(p.a_s) + m0 * srow : nullptr, MX ? rows * srow : 0);
+  // LDS: the sums of all wavefronts, then each one's codes and activations
+  float* const part = reinterpret_cast<float*>(gv_lds);
+  uint8_t* const lw = gv_lds + nw * 1024 * MT + wv * S::LDS;
+  uint8_t* const la = lw + 16 * S::WROW;
 
+  const int tile0 = blockIdx.x * p.tiles, tiles = min(p.tiles, (p.N + 15) / 16 - tile0);
+  const int steps = (K + KS - 1) / KS;
+  const int turns = (steps - wv + nw - 1) / nw;          // of this wavefront, at least one
+
+  uint4 cw[S::WLOADS], ca[S::ALOADS];
+  gv_uint2 sw, sa[MT];
   float4v acc[MT];
+  gv_uint2 fs, fa[MT];                          // scales of this lane's pieces
+  // iteration it: the codes of the one before go to LDS, its own are loaded,
+  // the ones in LDS are multiplied
+  int tile = 0, turn = 0, ptile = 0, pturn = 0;
+  for (bool first = true;; first = false) {
+    if (!first) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wv * 128; k0 < p.K; k0 += NW * 128) {
-    const int k = k0 + 32 * g;
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-    float s0 = 0.0f, s1 = 0.0f;
-    if (k < p.K) {
-      const uint8_t* src = wq + n * (p.K / 2) + k / 2;
-      const uint2 lo = *reinterpret_cast<const uint2*>(src);
-      c[0] = lo.x; c[1] = lo.y;
-      if (k + 16 < p.K) {
-        const uint2 hi = *reinterpret_cast<const uint2*>(src + 8);
-        c[2] = hi.x; c[3] = hi.y;
+      for (int i = 0; i < S::WLOADS; ++i) {
+        const int row = i * (1024 / S::WROW) + lane / (S::WROW / 16);
+        *reinterpret_cast<uint4*>(lw + row * S::WROW + 16 * ((lane % (S::WROW / 16)) ^ (row & 7))) = cw[i];
       }
-      if constexpr (MX) {
-        s0 = s1 = e8m0(wsc[n * (p.K / 32) + k / 32]);
+      fs[0] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sw[0]);
+      if constexpr (S::SB == 8) fs[1] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sw[1]);
+      if (turns > 1 || ptile == 0) {
+#pragma unroll
+        for (int i = 0; i < S::ALOADS; ++i) {
+          const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
+          *reinterpret_cast<uint4*>(la + row * S::AROW + 16 * ((lane % (S::AROW / 16)) ^ (row & 7))) = ca[i];
+        }
+        if constexpr (MX) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) fa[i][0] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sa[i][0]);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (tile < tiles) {
+      const int k0 = (turn * nw + wv) * KS;
+      const int n0 = (tile0 + tile) * 16;
+      const int64_t row0 = expert * p.N + n0;
+      const uint32_t nr = min(16, p.N - n0);
+      const __amdgpu_buffer_rsrc_t wq = raw_buffer(p.w_q + row0 * wrow, nr * wrow);
+      const __amdgpu_buffer_rsrc_t ws = raw_buffer(p.w_s + row0 * srow, nr * srow);
+      if (K % 32 == 0) {
+#pragma unroll
+        for (int i = 0; i < S::WLOADS; ++i) {
+          const int row = i * (1024 / S::WROW) + lane / (S::WROW / 16);
+          const int k = k0 + 32 * (lane % (S::WROW / 16));
+          cw[i] = buffer_load16(wq, k < K ? row * wrow + k / 2 : kGvNone);
+        }
       } else {
-        s0 = __builtin_amdgcn_cvt_f32_fp8(wsc[n * (p.K / 16) + k / 16], 0);
-        if (k + 16 < p.K) s1 = __builtin_amdgcn_cvt_f32_fp8(wsc[n * (p.K / 16) + k / 16 + 1], 0);
+        // a row's last 16 codes stand alone in front of the next row
+#pragma unroll
+        for (int i = 0; i < S::WLOADS; ++i) {
+          const int row = i * (1024 / S::WROW) + lane / (S::WROW / 16);
+          const int k = k0 + 32 * (lane % (S::WROW / 16));
+          const gv_uint2 lo = __builtin_amdgcn_raw_buffer_load_b64(wq, k < K ? row * wrow + k / 2 : kGvNone, 0, 0);
+          const gv_uint2 hi = __builtin_amdgcn_raw_buffer_load_b64(wq, k + 16 < K ? row * wrow + k / 2 + 8 : kGvNone, 0, 0);
+          cw[i] = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+        }
+      }
+      const int ks = k0 + (lane & 3) * (KS / 4);
+      sw = load_scales<S::SB, G>(ws, (lane >> 2) * srow + ks / G, ks, K);
+      // with one turn the activations of the first tile serve all
+      if (turns > 1 || tile == 0) {
+#pragma unroll
+        for (int i = 0; i < S::ALOADS; ++i) {
+          constexpr int E = 16 * 32 / ActBytes<AF>::n;           // activations of 16 bytes
+          const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
+          const int c = lane % (S::AROW / 16);
+          const uint32_t off = row * arow + (uint32_t)k0 * ActBytes<AF>::n / 32 + 16 * c;
+          ca[i] = buffer_load16(aq, k0 + E * c < K ? off : kGvNone);
+        }
+        if constexpr (MX) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            sa[i] = load_scales<S::SB, G>(as, (16 * i + (lane >> 2)) * srow + ks / G, ks, K);
+        }
       }
     }
+    if (!first) {
+      if (pturn == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const gv_bf16x8 w = decode_w8(c[j], j < 2 ? s0 : s1);
+        for (int i = 0; i < MT; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + r;
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(load_a8<AF>(p, m, m < rows, k + 8 * j), w, acc[i], 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const int piece = U * g + u;            // 32 elements of the step
+        const uint4 c = *reinterpret_cast<const uint4*>(lw + r * S::WROW + 16 * (piece ^ (r & 7)));
+        uint4 a[MT][ActBytes<AF>::loads];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int row = min(16 * i + r, rows - 1);            // rows past the last: never stored
+#pragma unroll
+          for (int l = 0; l < ActBytes<AF>::loads; ++l)
+            a[i][l] = *reinterpret_cast<const uint4*>(la + row * S::AROW + 16 * ((piece * ActBytes<AF>::loads + l) ^ (row & 7)));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t cj = j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w;
+          GvFrag<AF> w;
+          if constexpr (MX) {
+            w = decode_mx4<AF>(cj, e8m0((fs[0] >> (8 * u)) & 0xFFu));
+          } else {
+            const int b = 2 * u + (j >> 1);     // the 16-element group among the lane's
+            w = decode_nv<AF>(cj, __builtin_amdgcn_cvt_f32_fp8((int)(fs[b >> 2] >> (8 * (b & 3))), 0));
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i] = gv_mfma<AF>(decode_act<AF>(a[i], MX ? e8m0((fa[i][0] >> (8 * u)) & 0xFFu) : 0.0f, j), w, acc[i]);
+        }
       }
     }
+    if (!first && pturn == turns - 1) {
+      // register e of lane l: row 4 (l / 16) + e, feature l % 16
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[(wv * 16 * MT + 16 * i + 4 * g + e) * 16 + r] = acc[i][e];
+      wait_lgkm_barrier();                      // leaves the loads in flight
+      const int n0 = (tile0 + ptile) * 16;
+      for (int o = threadIdx.x; o < 256 * MT; o += blockDim.x) {
+        const int mr = o >> 4, nc = o & 15;
+        if (mr >= rows || n0 + nc >= p.N) continue;
+        float s = part[o];
+        for (int w = 1; w < nw; ++w) s = s + part[w * 256 * MT + o];
+        const int64_t m = m0 + mr;
+        if constexpr (AF == kActBf16) s = s * p.w_ts[1];
+        if constexpr (AF == kActInt8) s = s * (static_cast<const float*>(p.a_s)[m] * p.w_ts[1]);
+        if (p.bias) s = s + p.bias[expert * p.N + n0 + nc];
+        if (p.out_f32)
+          static_cast<float*>(p.y)[m * p.ldy + n0 + nc] = s;
+        else
+          static_cast<__bf16*>(p.y)[m * p.ldy + n0 + nc] = (__bf16)s;
+      }
+      if (ptile + 1 == tiles) return;
+      wait_lgkm_barrier();                      // the sums are read before the next tile's
+    }
+    ptile = tile;
+    pturn = turn;
+    if (++turn == turns) {
+      turn = 0;
+      ++tile;
+    }
   }
-  // register e of lane l: row 4 (l / 16) + e, feature l % 16
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[wv][16 * i + 4 * g + e][r] = acc[i][e];
-  __syncthreads();
-  const int mr = threadIdx.x >> 4, nc = threadIdx.x & 15;
-  const int64_t m = m0 + mr;
-  if (mr < MT * 16 && m < rows && n0 + nc < p.N) {
-    float s = part[0][mr][nc];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) s = s + part[w][mr][nc];
-    if constexpr (AF == kActBf16) s = s * p.w_ts[1];
-    if constexpr (AF == kActInt8) s = s * (static_cast<const float*>(p.a_s)[m] * p.w_ts[1]);
-    if (p.bias) s = s + p.bias[expert * p.N + n0 + nc];
-    if (p.out_f32)
-      static_cast<float*>(p.y)[m * p.ldy + n0 + nc] = s;
-    else
-      static_cast<__bf16*>(p.y)[m * p.ldy + n0 + nc] = (__bf16)s;
-  }
+}
+
+template <int AF, int MR>
+static hipError_t launch_tiles(GemvParams p, int gy, int tiles, int64_t max_lds, hipStream_t st) {
+  using S = GvStep<AF, MR>;
+  p.tiles = tiles;
+  // wavefronts: one per step of K while they fit, then evenly loaded ones
+  const int steps = (p.K + S::KS - 1) / S::KS, wave = S::LDS + 1024 * S::MT;
+  const int most = (int)std::min<int64_t>(S::WAVES, max_lds / wave);
+  const int turns = (steps + most - 1) / most, nw = (steps + turns - 1) / turns;
+  const hipError_t e = allow_lds_once<AF * 64 + MR>(reinterpret_cast<const void*>(&qgemv_kernel<AF, MR>), kGvMaxLds);
+  if (e != hipSuccess) return e;
+  const int64_t gx = ((p.N + 15) / 16 + tiles - 1) / tiles;
+  hipLaunchKernelGGL((qgemv_kernel<AF, MR>), dim3((unsigned)gx, (unsigned)gy), dim3(64 * nw), nw * wave, st, p);
+  return hipGetLastError();
 }
 
 template <int AF>
 static hipError_t launch_gemv(const GemvParams& p, hipStream_t st) {
-  const unsigned gx = (unsigned)((p.N + 15) / 16);
-  if (p.offsets)
-    hipLaunchKernelGGL((qgemv_kernel<AF, 2>), dim3(gx, (unsigned)(p.M / 32 + p.E)), dim3(512), 0, st, p);
-  else if (p.M <= 16)
-    hipLaunchKernelGGL((qgemv_kernel<AF, 1>), dim3(gx), dim3(512), 0, st, p);
-  else
-    hipLaunchKernelGGL((qgemv_kernel<AF, 2>), dim3(gx), dim3(512), 0, st, p);
-  return hipGetLastError();
+  // one workgroup a compute unit when there are no more: all of its LDS
+  const int64_t lds = (p.N + 15) / 16 > device_cu_count() ? kGvMaxLds / 2 : kGvMaxLds;
+  if (p.M <= 4) return launch_tiles<AF, 4>(p, 1, 1, lds, st);
+  return p.M <= 16 ? launch_tiles<AF, 16>(p, 1, 1, lds, st) : launch_tiles<AF, 32>(p, 1, 1, lds, st);
 }
 
 hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t* w_q, const uint8_t* w_s,
@@ -203,7 +423,13 @@ hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t
   p.w_q = w_q; p.w_s = w_s; p.bias = bias; p.offsets = offsets;
   p.y = y; p.ldy = ldy; p.out_f32 = out_dtype == 1;
   p.M = (int32_t)T; p.N = (int32_t)N; p.K = (int32_t)K; p.E = (int32_t)E;
-  return a_fp8 ? launch_gemv<kActMx8>(p, st) : launch_gemv<kActMx4>(p, st);
+  const int avg = (int)(T / E);
+  if (avg <= 8) {
+    const int gy = (int)(T / 16 + E);
+    return a_fp8 ? launch_tiles<kActMx8, 16>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 16>(p, gy, 4, kGvMaxLds / 2, st);
+  }
+  const int gy = (int)(T / 32 + E);
+  return a_fp8 ? launch_tiles<kActMx8, 32>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 32>(p, gy, 4, kGvMaxLds / 2, st);
 }
 
 }  // namespace vdtq
