@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libvdtq.so")
 BENCH_LIB = os.path.join(HERE, "libvdtq_bench.so")
 BENCH_SOURCES = ["bench_stream.hip"]
 SOURCES = ["hadamard_quantize.hip", "qgemm.hip", "qgemm_mx.hip", "qgemm_w4a16.hip", "block_stats.hip",
-           "rmsnorm_quantize.hip", "qgemv.hip", "api.cpp", "dmpq.cpp"]
+           "rmsnorm_quantize.hip", "qgemv.hip", "qgemm_mx_grouped.hip", "api.cpp", "dmpq.cpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

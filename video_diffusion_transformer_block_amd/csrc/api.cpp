@@ -401,9 +401,11 @@ int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, 
   if (!offsets_dev || !aligned(offsets_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned offsets", name);
   if (!aligned(a_s_dev, 4) || !aligned(w_s_dev, 4)) return fail(VDTQ_EINVAL, "%s: scales need 4 bytes alignment", name);
   if (K % 128) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is not a multiple of 128", name, (long long)K);
-  hipError_t e = vdtq::launch_qgemm_mx_grouped(a_fmt == VDTQ_FMT_MXFP8, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev,
-                                               offsets_dev, E, y_dev, ldy, out_dtype, T, N, K,
-                                               static_cast<hipStream_t>(stream));
+  // row tiles (of 16 rows at least) and feature tiles (of 16) are counted in 31 bits
+  if ((T / 16 + E) * ((N + 15) / 16) > kI32) return fail(VDTQ_EUNSUPPORTED, "%s: too many output tiles", name);
+  const vdtq::MxGrouped q{a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, offsets_dev, y_dev, ldy,
+                          (int32_t)T, (int32_t)N, (int32_t)K, (int32_t)E, out_dtype == VDTQ_OUT_F32};
+  hipError_t e = vdtq::launch_qgemm_mx_grouped(a_fmt == VDTQ_FMT_MXFP8, q, static_cast<hipStream_t>(stream));
   return hip_status(e, "qgemm_mx_grouped launch");
 }
 

@@ -88,15 +88,21 @@ static hipError_t allow_lds_once(const void* kernel, int bytes) {
   return e;
 }
 
-// Rows grouped by expert: tiles of 256 x 256 (qgemm_mx.hip), and the choice
-// between them and the few-row kernel.
-hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
-                                       const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E,
-                                       void* y, int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K,
-                                       hipStream_t st);
-hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
-                                   const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E, void* y,
-                                   int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, hipStream_t st);
+// Rows grouped by expert (MX operands): the choice of a kernel
+// (qgemm_mx_grouped.hip) and the ones it chooses between: 256 x 256 tiles
+// (qgemm_mx.hip) and sums of exact products (qgemv.hip).
+struct MxGrouped {
+  const uint8_t *a_q, *a_s, *w_q, *w_s;
+  const float* bias;             // [E][N] or NULL
+  const int32_t* offsets;        // [E + 1]
+  void* y;
+  int64_t ldy;
+  int32_t T, N, K, E;
+  int32_t out_f32;
+};
+hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st);
+hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const MxGrouped& q, hipStream_t st);
+hipError_t launch_qgemm_mx_grouped_exact(bool a_fp8, const MxGrouped& q, hipStream_t st);
 
 size_t bs_workspace_bytes(int64_t n);
 hipError_t launch_block_stats(const void* in, const void* out, const void* dprev, void* dnew,

@@ -547,25 +547,22 @@ hipError_t launch_qgemm_mx_quant(bool a_fp8, const uint8_t* a_q, const uint8_t* 
   return out_fp8 ? launch_mx_quant<false, false, 2>(p, st) : launch_mx_quant<false, false, 1>(p, st);
 }
 
-hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
-                                       const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E,
-                                       void* y, int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K,
-                                       hipStream_t st) {
+hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const MxGrouped& q, hipStream_t st) {
   GemmParams p{};
-  p.a_q = a_q; p.a_s = a_s;
-  p.w_q = w_q; p.w_s = w_s;
-  p.bias = bias; p.y = y; p.ldy = ldy;
-  p.M = (int32_t)T; p.N = (int32_t)N; p.K = (int32_t)K;
-  p.out_f32 = out_dtype == 1;
+  p.a_q = q.a_q; p.a_s = q.a_s;
+  p.w_q = q.w_q; p.w_s = q.w_s;
+  p.bias = q.bias; p.y = q.y; p.ldy = q.ldy;
+  p.M = q.T; p.N = q.N; p.K = q.K;
+  p.out_f32 = q.out_f32;
   p.tiles_n = (p.N + 255) / 256;
   p.nk = p.K / BK;
-  p.offsets = offsets;
-  p.experts = (int32_t)E;
-  const unsigned grid = (unsigned)((T / 256 + E) * p.tiles_n);
+  p.offsets = q.offsets;
+  p.experts = q.E;
+  const unsigned grid = (unsigned)((q.T / 256 + q.E) * p.tiles_n);
   // the device-side staged_store_ok, for every expert's bias and rows
   const bool staged = !p.out_f32 && (p.N % 8) == 0 && (p.ldy % 8) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 &&
                       (!p.bias || (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0);
-  if (mx_quads(K)) {
+  if (mx_quads(q.K)) {
     if (a_fp8) return staged ? launch_mx_grouped<true, true, true>(p, grid, st) : launch_mx_grouped<true, true, false>(p, grid, st);
     return staged ? launch_mx_grouped<false, true, true>(p, grid, st) : launch_mx_grouped<false, true, false>(p, grid, st);
   }

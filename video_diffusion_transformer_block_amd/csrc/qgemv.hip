@@ -127,23 +127,22 @@ __device__ __forceinline__ void decode_i8(uint32_t lo, uint32_t hi, uint32_t (&o
   o[3] = __builtin_bit_cast(uint32_t, (half2v)(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, y, 0x04030402u)) - off));
 }
 
-// bytes of 32 activations, and the 16-byte loads they take
+// bytes of 32 activations, and the activations of a 16-byte load
 template <int AF>
 struct ActBytes {
   static constexpr int n = AF == kActBf16 ? 64 : AF == kActMx4 ? 16 : 32;
-  static constexpr int loads = n / 16;
+  static constexpr int per_load = 16 * 32 / n;
 };
 
-// activations 8 j .. 8 j + 7 of the 32 in w
+// activations 8 j .. 8 j + 7 of 16 bytes
 template <int AF>
-__device__ __forceinline__ GvFrag<AF> decode_act(const uint4 (&w)[ActBytes<AF>::loads], float sc, int j) {
+__device__ __forceinline__ GvFrag<AF> decode_act(const uint4& v, float sc, int j) {
   GvFrag<AF> o;
   if constexpr (AF == kActBf16) {
-    o.w[0] = w[j].x; o.w[1] = w[j].y; o.w[2] = w[j].z; o.w[3] = w[j].w;
+    o.w[0] = v.x; o.w[1] = v.y; o.w[2] = v.z; o.w[3] = v.w;
   } else if constexpr (AF == kActMx4) {
-    o = decode_mx4<AF>(j == 0 ? w[0].x : j == 1 ? w[0].y : j == 2 ? w[0].z : w[0].w, sc);
+    o = decode_mx4<AF>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc);
   } else {
-    const uint4 v = w[j >> 1];
     const uint32_t lo = j & 1 ? v.z : v.x, hi = j & 1 ? v.w : v.y;
     if constexpr (AF == kActInt8) {
       decode_i8(lo, hi, o.w);
@@ -167,7 +166,13 @@ template <int AF, int MR>
 struct GvStep {
   static constexpr bool MX = AF >= kActMx8;
   static constexpr int MT = (MR + 15) / 16;     // tiles of 16 rows
-  static constexpr int KS = (AF == kActBf16 || MR == 32) ? 256 : 512;  // K
+  // activations go to LDS decoded to 16 bits where they are few (every
+  // fragment then needs no decoding: 11.0 -> 10.2 us for one INT8 row,
+  // K = 3072, N = 12288), as they are from 16 rows on, where that would
+  // double the LDS and leave room for fewer wavefronts (64 rows over 32
+  // experts, K = 1920, N = 7680: 52 -> 70 us)
+  static constexpr bool DECODED = AF == kActBf16 || MR == 4;
+  static constexpr int KS = MR == 4 || (MR == 16 && AF != kActBf16) ? 512 : 256;   // K
   static constexpr int WAVES = MR == 32 ? 8 : 16;                      // at most
   static constexpr int U = KS / 128;            // 32-element pieces a lane takes
   static constexpr int WROW = KS / 2;           // code bytes of a feature
@@ -175,7 +180,8 @@ struct GvStep {
   static constexpr int AROW = KS * ActBytes<AF>::n / 32;
   static constexpr int ALOADS = (MR * AROW + 1023) / 1024;
   static constexpr int ALOAD_ROWS = 1024 / AROW;
-  static constexpr int LDS = 16 * WROW + ALOADS * 1024;                // bytes of a wavefront
+  static constexpr int DROW = DECODED ? 2 * KS : AROW;                 // a row of A in LDS
+  static constexpr int LDS = 16 * WROW + MR * DROW;                    // bytes of a wavefront
   static constexpr int SB = KS / 4 / (MX ? 32 : 16);   // scale bytes of a lane
 };
 
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
   using S = GvStep<AF, MR>;
   constexpr int MT = S::MT;
   constexpr bool MX = S::MX;
-  constexpr int G = MX ? 32 : 16, KS = S::KS, U = S::U;
+  constexpr int G = MX ? 32 : 16, KS = S::KS, U = S::U, E = ActBytes<AF>::per_load;
   extern __shared__ __attribute__((aligned(16))) uint8_t gv_lds[];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -231,9 +237,10 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
   const int turns = (steps - wv + nw - 1) / nw;          // of this wavefront, at least one
 
   uint4 cw[S::WLOADS], ca[S::ALOADS];
-  gv_uint2 sw, sa[MT];
+  uint32_t sa[S::ALOADS];                       // MX, decoded: the scale byte of ca
+  uint32_t ra[MT], fa[MT];                      // MX, not decoded: scales as loaded, and of this lane's pieces
+  gv_uint2 sw, fs;                              // weight scales as loaded, and of this lane's pieces
   float4v acc[MT];
-  gv_uint2 fs, fa[MT];                          // scales of this lane's pieces
   // iteration it: the codes of the one before go to LDS, its own are loaded,
   // the ones in LDS are multiplied
   int tile = 0, turn = 0, ptile = 0, pturn = 0;
@@ -251,11 +258,20 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
 #pragma unroll
         for (int i = 0; i < S::ALOADS; ++i) {
           const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
-          *reinterpret_cast<uint4*>(la + row * S::AROW + 16 * ((lane % (S::AROW / 16)) ^ (row & 7))) = ca[i];
-        }
-        if constexpr (MX) {
+          if constexpr (!S::DECODED) {
+            *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * ((lane % (S::AROW / 16)) ^ (row & 7))) = ca[i];
+          } else if (MR * S::AROW >= 1024 || row < MR) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) fa[i][0] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sa[i][0]);
+            for (int j = 0; j < E / 8; ++j) {
+              const GvFrag<AF> d = decode_act<AF>(ca[i], MX ? e8m0(sa[i]) : 0.0f, j);
+              const int piece = lane % (S::AROW / 16) * (E / 8) + j;
+              *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * (piece ^ (row & 7))) = make_uint4(d.w[0], d.w[1], d.w[2], d.w[3]);
+            }
+          }
+        }
+        if constexpr (MX && !S::DECODED) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) fa[i] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), ra[i]);
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -292,16 +308,15 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
       if (turns > 1 || tile == 0) {
 #pragma unroll
         for (int i = 0; i < S::ALOADS; ++i) {
-          constexpr int E = 16 * 32 / ActBytes<AF>::n;           // activations of 16 bytes
           const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
-          const int c = lane % (S::AROW / 16);
-          const uint32_t off = row * arow + (uint32_t)k0 * ActBytes<AF>::n / 32 + 16 * c;
-          ca[i] = buffer_load16(aq, k0 + E * c < K ? off : kGvNone);
+          const int k = k0 + E * (lane % (S::AROW / 16));
+          ca[i] = buffer_load16(aq, k < K ? row * arow + (uint32_t)k / 32 * ActBytes<AF>::n + (uint32_t)k % 32 * ActBytes<AF>::n / 32 : kGvNone);
+          if constexpr (MX && S::DECODED)
+            sa[i] = __builtin_amdgcn_raw_buffer_load_b8(as, k < K ? row * srow + k / 32 : kGvNone, 0, 0);
         }
-        if constexpr (MX) {
+        if constexpr (MX && !S::DECODED) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            sa[i] = load_scales<S::SB, G>(as, (16 * i + (lane >> 2)) * srow + ks / G, ks, K);
+          for (int i = 0; i < MT; ++i) ra[i] = load_scales<S::SB, G>(as, (16 * i + (lane >> 2)) * srow + ks / G, ks, K)[0];
         }
       }
     }
@@ -314,13 +329,13 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
       for (int u = 0; u < U; ++u) {
         const int piece = U * g + u;            // 32 elements of the step
         const uint4 c = *reinterpret_cast<const uint4*>(lw + r * S::WROW + 16 * (piece ^ (r & 7)));
-        uint4 a[MT][ActBytes<AF>::loads];
+        uint4 raw[MT][32 / E];                  // the piece's activations, not decoded
+        if constexpr (!S::DECODED) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int row = min(16 * i + r, rows - 1);            // rows past the last: never stored
+          for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int l = 0; l < ActBytes<AF>::loads; ++l)
-            a[i][l] = *reinterpret_cast<const uint4*>(la + row * S::AROW + 16 * ((piece * ActBytes<AF>::loads + l) ^ (row & 7)));
+            for (int l = 0; l < 32 / E; ++l)
+              raw[i][l] = *reinterpret_cast<const uint4*>(la + (16 * i + r) * S::DROW + 16 * ((32 / E * piece + l) ^ (r & 7)));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -333,8 +348,17 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
             w = decode_nv<AF>(cj, __builtin_amdgcn_cvt_f32_fp8((int)(fs[b >> 2] >> (8 * (b & 3))), 0));
           }
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[i] = gv_mfma<AF>(decode_act<AF>(a[i], MX ? e8m0((fa[i][0] >> (8 * u)) & 0xFFu) : 0.0f, j), w, acc[i]);
+          for (int i = 0; i < MT; ++i) {
+            GvFrag<AF> a;
+            if constexpr (S::DECODED) {
+              const int row = min(16 * i + r, MR - 1);          // of 4 rows: the last again, never stored
+              const uint4 v = *reinterpret_cast<const uint4*>(la + row * S::DROW + 16 * ((4 * piece + j) ^ (row & 7)));
+              a = GvFrag<AF>{{v.x, v.y, v.z, v.w}};
+            } else {
+              a = decode_act<AF>(raw[i][8 * j / E], MX ? e8m0((fa[i] >> (8 * u)) & 0xFFu) : 0.0f, j % (E / 8));
+            }
+            acc[i] = gv_mfma<AF>(a, w, acc[i]);
+          }
         }
       }
     }
@@ -412,23 +436,18 @@ hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t
   }
 }
 
-hipError_t launch_qgemm_mx_grouped(bool a_fp8, const uint8_t* a_q, const uint8_t* a_s, const uint8_t* w_q,
-                                   const uint8_t* w_s, const float* bias, const int32_t* offsets, int64_t E, void* y,
-                                   int64_t ldy, int out_dtype, int64_t T, int64_t N, int64_t K, hipStream_t st) {
-  if (T == 0 || N == 0) return hipSuccess;
-  if (T / E >= 64 && (out_dtype == 0 || !a_fp8))
-    return launch_qgemm_mx_grouped_256(a_fp8, a_q, a_s, w_q, w_s, bias, offsets, E, y, ldy, out_dtype, T, N, K, st);
+hipError_t launch_qgemm_mx_grouped_exact(bool a_fp8, const MxGrouped& q, hipStream_t st) {
   GemvParams p{};
-  p.a_q = a_q; p.a_s = a_s;
-  p.w_q = w_q; p.w_s = w_s; p.bias = bias; p.offsets = offsets;
-  p.y = y; p.ldy = ldy; p.out_f32 = out_dtype == 1;
-  p.M = (int32_t)T; p.N = (int32_t)N; p.K = (int32_t)K; p.E = (int32_t)E;
-  const int avg = (int)(T / E);
-  if (avg <= 8) {
-    const int gy = (int)(T / 16 + E);
+  p.a_q = q.a_q; p.a_s = q.a_s;
+  p.w_q = q.w_q; p.w_s = q.w_s; p.bias = q.bias; p.offsets = q.offsets;
+  p.y = q.y; p.ldy = q.ldy; p.out_f32 = q.out_f32;
+  p.M = q.T; p.N = q.N; p.K = q.K; p.E = q.E;
+  // 4 feature tiles a workgroup: finding its rows takes about as long as one
+  if (q.T / q.E <= 8) {
+    const int gy = q.T / 16 + q.E;
     return a_fp8 ? launch_tiles<kActMx8, 16>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 16>(p, gy, 4, kGvMaxLds / 2, st);
   }
-  const int gy = (int)(T / 32 + E);
+  const int gy = q.T / 32 + q.E;
   return a_fp8 ? launch_tiles<kActMx8, 32>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 32>(p, gy, 4, kGvMaxLds / 2, st);
 }
 
