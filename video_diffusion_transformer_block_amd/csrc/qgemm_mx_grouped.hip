@@ -5,8 +5,7 @@
 // instruction of qgemm_mx.hip.  With few rows an expert the time is that of
 // reading its weights once.
 //
-// A workgroup owns a tile of MR (16 or 32) rows of one expert and `tiles`
-// blocks of 16 features one after the other.  Its wavefronts split K, 512
+// A workgroup owns a tile of 16 rows of one expert and `tiles` blocks of 16 features one after the other.  Its wavefronts split K, 512
 // elements each: a wavefront keeps its part of the rows in registers as
 // operands of v_mfma_scale_f32_16x16x128_f8f6f4 and streams its part of the
 // weights through a ring of D blocks in LDS of its own by direct-to-LDS loads
@@ -19,6 +18,7 @@
 #include "device_common.h"
 #include "launch.h"
 #include "lds_dma.h"
+#include "qgemm_common.h"
 #include "row_groups.h"
 
 namespace vdtq {
@@ -33,7 +33,8 @@ constexpr int kMgSlot = kMgCodes + 256;         // 16 scale bytes of 16 features
 constexpr int kMgLoads = kMgCodes / 1024 + 1;
 constexpr uint32_t kMgNone = 0xFFFFFFF0u;       // an offset past every buffer: reads zeros
 
-constexpr int D = 2;                            // blocks of the ring
+constexpr int kMgRows = 16;
+constexpr int D = 2;                            // blocks of the ring (3 and 4: 8 % and 10 % slower, fewer workgroups fit)
 constexpr int kMgMaxLds = 160 * 1024;
 
 struct MgParams {
@@ -41,25 +42,24 @@ struct MgParams {
   int32_t tiles;             // feature blocks of a workgroup
 };
 
-template <bool A8, int MR, int TURNS>
+template <bool A8, int TURNS>
 __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp) {
-  constexpr int MT = MR / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t mg_lds[];
   const MxGrouped& p = mp.q;
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int K = p.K, N = p.N;
-  const RowTile t = row_tile(p.offsets, p.E, p.T, MR, blockIdx.y);
+  const RowTile t = row_tile(p.offsets, p.E, p.T, kMgRows, blockIdx.y);
   if (t.rows <= 0) return;                      // the grid is an upper bound
-  const int rows = min(t.rows, MR);
+  const int rows = min(t.rows, kMgRows);
   const int tile0 = blockIdx.x * mp.tiles, tiles = min(mp.tiles, (N + 15) / 16 - tile0);
   const uint32_t wrow = K / 2, srow = K / 32, arow = A8 ? K : K / 2;
 
-  // LDS: two sets of sums [wavefront][16 MT][16], the bias, the rings
+  // LDS: two sets of sums [wavefront][16][16], the bias, the rings
   float* const part = reinterpret_cast<float*>(mg_lds);
-  float* const bias = part + 2 * nw * 256 * MT;
-  const uint32_t ring0 = (uint32_t)(2 * nw * 1024 * MT + mp.tiles * 64 + wv * D * kMgSlot);
+  float* const bias = part + 2 * nw * 256;
+  const uint32_t ring0 = (uint32_t)(2 * nw * 1024 + mp.tiles * 64 + wv * D * kMgSlot);
   const uint8_t* const ring = mg_lds + ring0;
   const uint32_t ringa = (uint32_t)(size_t)(lds_void_t*)mg_lds + ring0;
 
@@ -93,33 +93,29 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
   // or upper half by (l / 16) % 2.
   const __amdgpu_buffer_rsrc_t aq = raw_buffer(p.a_q + (int64_t)t.row0 * arow, rows * arow);
   const __amdgpu_buffer_rsrc_t as = raw_buffer(p.a_s + (int64_t)t.row0 * srow, rows * srow);
-  mg_int8 xa[TURNS][MT][4];
-  uint32_t fa[TURNS][MT];
+  mg_int8 xa[TURNS][4];
+  uint32_t fa[TURNS];
 #pragma unroll
   for (int turn = 0; turn < TURNS; ++turn) {
     const int k0 = (turn * nw + wv) * kMgStep;
+    auto piece = [&](int k, uint32_t bytes) {
+      const uint4 v = buffer_load16(aq, k < K ? r * arow + bytes : kMgNone);
+      return mg_int4{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+    };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const uint32_t row = 16 * i + r;
-      auto piece = [&](int k, uint32_t bytes) {
-        const uint4 v = buffer_load16(aq, k < K ? row * arow + bytes : kMgNone);
-        return mg_int4{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
-      };
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (A8) {
-          const int ka = k0 + 32 * (4 * (g >> 1) + u) + 16 * (g & 1), kb = ka + 256;
-          const mg_int4 lo = piece(ka, ka), hi = piece(kb, kb);
-          xa[turn][i][u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-          const int k = k0 + 32 * (4 * g + u);
-          const mg_int4 v = piece(k, k / 2);
-          xa[turn][i][u] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-        }
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (A8) {
+        const int ka = k0 + 32 * (4 * (g >> 1) + u) + 16 * (g & 1), kb = ka + 256;
+        const mg_int4 lo = piece(ka, ka), hi = piece(kb, kb);
+        xa[turn][u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      } else {
+        const int k = k0 + 32 * (4 * g + u);
+        const mg_int4 v = piece(k, k / 2);
+        xa[turn][u] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
       }
-      const int k = k0 + 128 * g;
-      fa[turn][i] = __builtin_amdgcn_raw_buffer_load_b32(as, k < K ? row * srow + k / 32 : kMgNone, 0, 0);
     }
+    const int k = k0 + 128 * g;
+    fa[turn] = __builtin_amdgcn_raw_buffer_load_b32(as, k < K ? r * srow + k / 32 : kMgNone, 0, 0);
   }
   if (p.bias) {
     for (int o = threadIdx.x; o < 16 * tiles; o += blockDim.x)
@@ -130,9 +126,7 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
   __builtin_amdgcn_s_waitcnt(0x0F70);           // vmcnt(0)
 
   for (int tile = 0; tile < tiles; ++tile) {
-    float4v acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    float4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int turn = 0; turn < TURNS; ++turn) {
       // the unit has landed when only the D - 1 after it are in flight
@@ -147,11 +141,9 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
         c[u] = *reinterpret_cast<const mg_int4*>(slot + r * (kMgStep / 2) + 16 * ((4 * g + u) ^ (r & 7)));
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              xa[turn][i][u], __builtin_shufflevector(c[u], c[u], 0, 1, 2, 3, -1, -1, -1, -1), acc[i], A8 ? 0 : 4, 4, 0,
-              (int)(fa[turn][i] >> (8 * u)), 0, (int)(fs >> (8 * u)));
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            xa[turn][u], __builtin_shufflevector(c[u], c[u], 0, 1, 2, 3, -1, -1, -1, -1), acc, A8 ? 0 : 4, 4, 0,
+            (int)(fa[turn] >> (8 * u)), 0, (int)(fs >> (8 * u)));
       // every read of the slot is done: its next unit
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (unit + D < tiles * TURNS) issue(unit + D);
@@ -159,18 +151,16 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
     // register e of lane l: row 4 (l / 16) + e, feature l % 16.  Two sets of
     // sums: a wavefront past a block's barrier cannot reach the block after
     // the next before all have read this one's
-    float* const sums = part + (tile & 1) * nw * 256 * MT;
+    float* const sums = part + (tile & 1) * nw * 256;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sums[(wv * 16 * MT + 16 * i + 4 * g + e) * 16 + r] = acc[i][e];
+    for (int e = 0; e < 4; ++e) sums[(wv * 16 + 4 * g + e) * 16 + r] = acc[e];
     wait_lgkm_barrier();
     const int n0 = (tile0 + tile) * 16;
-    for (int o = threadIdx.x; o < 256 * MT; o += blockDim.x) {
+    for (int o = threadIdx.x; o < 256; o += blockDim.x) {
       const int mr = o >> 4, nc = o & 15;
       if (mr >= rows || n0 + nc >= N) continue;
       float s = sums[o];
-      for (int w = 1; w < nw; ++w) s = s + sums[w * 256 * MT + o];
+      for (int w = 1; w < nw; ++w) s = s + sums[w * 256 + o];
       if (p.bias) s = s + bias[16 * tile + nc];
       const int64_t at = (int64_t)(t.row0 + mr) * p.ldy + n0 + nc;
       if (p.out_f32)
@@ -181,39 +171,293 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
   }
 }
 
-static int stream_lds(int nw, int MR, int tiles) { return nw * (128 * MR + D * kMgSlot) + 64 * tiles; }
-
-template <bool A8, int MR, int TURNS>
+template <bool A8, int TURNS>
 static hipError_t launch_stream(const MxGrouped& q, int nw, hipStream_t st) {
   // feature blocks of a workgroup: up to 8, as long as every compute unit has
-  // two workgroups (8 against 4 or 16: within 10 %)
+  // two workgroups (4 or 16 of them: within 10 %)
   const int blocks = (q.N + 15) / 16;
   const int64_t wgs = (int64_t)blocks * std::min(q.E, q.T);
-  const char* tv = getenv("TILES");
-  const MgParams p{q, tv ? atoi(tv) : (int)std::max<int64_t>(1, std::min<int64_t>(8, wgs / (2 * device_cu_count())))};
-  const hipError_t e = allow_lds_once<A8 * 256 + MR * 4 + TURNS>(reinterpret_cast<const void*>(&mx_stream_kernel<A8, MR, TURNS>), kMgMaxLds);
+  const MgParams p{q, (int)std::max<int64_t>(1, std::min<int64_t>(8, wgs / (2 * device_cu_count())))};
+  const hipError_t e = allow_lds_once<A8 * 2 + TURNS - 1>(reinterpret_cast<const void*>(&mx_stream_kernel<A8, TURNS>), kMgMaxLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((mx_stream_kernel<A8, MR, TURNS>), dim3((unsigned)((blocks + p.tiles - 1) / p.tiles), (unsigned)(q.T / MR + q.E)),
-                     dim3(64 * nw), stream_lds(nw, MR, p.tiles), st, p);
+  const int lds = nw * (2 * 1024 + D * kMgSlot) + 64 * p.tiles;
+  hipLaunchKernelGGL((mx_stream_kernel<A8, TURNS>), dim3((unsigned)((blocks + p.tiles - 1) / p.tiles), (unsigned)(q.T / kMgRows + q.E)),
+                     dim3(64 * nw), lds, st, p);
   return hipGetLastError();
 }
 
 template <bool A8>
 static hipError_t stream(const MxGrouped& q, hipStream_t st) {
   const int steps = (q.K + kMgStep - 1) / kMgStep;
-  if (q.T / q.E > 8 && stream_lds(steps, 32, 8) <= kMgMaxLds) return launch_stream<A8, 32, 1>(q, steps, st);
-  if (steps <= kMgMaxWaves) return launch_stream<A8, 16, 1>(q, steps, st);
-  return launch_stream<A8, 16, 2>(q, (steps + 1) / 2, st);
+  if (steps <= kMgMaxWaves) return launch_stream<A8, 1>(q, steps, st);
+  return launch_stream<A8, 2>(q, (steps + 1) / 2, st);
+}
+
+// ------------------------------------------------------ tiles of BM x BN
+// Experts of middling row counts.  A workgroup of 4 wavefronts (2 x 2) owns
+// BM rows of one expert times BN features, several workgroups share a compute
+// unit: one's loads, barriers and epilogue pass under another's matrix
+// instructions.  K in stages of 128 through a ring of NS in LDS (the layout
+// and the direct-to-LDS loads of qgemm_mx.hip).  With three stages one barrier
+// a stage is enough: it says that the stage has landed for all and that all
+// are done with the one before, whose slot takes the next load; with two, the
+// fragments of a whole stage are read before a second barrier frees the slot.
+// Scales: 16 bytes a row are those of four stages; each stage's issue loads a
+// quarter of the rows of the next four (coalesced: a dword a row and stage
+// would take as many memory requests as the codes), into a ring of three.
+template <bool A8, int BM, int BN, int NS_>
+struct MgTile {
+  static constexpr int NS = NS_;
+  static constexpr int A = BM * (A8 ? 128 : 64), W = BN * 64;      // code bytes of a stage
+  static constexpr int NA = A / 4096, NW = W / 4096;               // loads of a wavefront
+  static constexpr int ROWS = BM + BN;
+  static constexpr int SL = (ROWS + 255) / 256;
+  static constexpr int LPS = NA + NW + SL;
+  static constexpr int STAGE = A + W;
+  static constexpr int SC = NS * STAGE;                            // scale ring: 3 x ROWS x 16
+  static constexpr int MAIN = SC + 3 * ROWS * 16;
+  static constexpr int TM = BM / 64, TN = BN / 64;                 // 32 x 32 blocks of a wavefront
+  static constexpr int OUTROW = BN + 16;                           // bytes of a wavefront's output row in LDS
+  static constexpr int OUT = 4 * (BM / 2) * OUTROW;
+  static constexpr int LDS = MAIN > OUT ? MAIN : OUT;
+  static constexpr int WGS = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;   // workgroups of a compute unit
+};
+
+template <bool A8, int BM, int BN, int NS, int WGS = MgTile<A8, BM, BN, NS>::WGS>
+__global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
+  using S = MgTile<A8, BM, BN, NS>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t mg_lds[];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv >> 1, wn = wv & 1, r32 = lane & 31, h = lane >> 5;
+  const int K = p.K, N = p.N, nk = K / 128;
+  const int tiles_n = (N + BN - 1) / BN;
+  const int total = row_tiles(p.offsets, p.E, p.T, BM) * tiles_n;
+  if ((int)blockIdx.x >= total) return;         // the grid is an upper bound
+  const int id = xcd_range_id(blockIdx.x, total);
+  // (quotients come from the vector unit: the bases of the loads need scalars)
+  const int along = __builtin_amdgcn_readfirstlane(id / tiles_n);
+  const RowTile t = row_tile(p.offsets, p.E, p.T, BM, along);
+  // the expert's tiles: groups of 8 row tiles walked along the features
+  const int first = t.row0 - (along - t.before) * BM, all = t.row0 + t.rows;
+  int tm, tn;
+  tile_coords(id - t.before * tiles_n, t.tiles, tiles_n, tm, tn);
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
+  const int row0 = first + tm * BM, rows = min(all - row0, BM);
+  const int n0 = tn * BN, feats = min(N - n0, BN);
+
+  const uint32_t arow = A8 ? K : K / 2, wrow = K / 2, srow = K / 32;
+  const uint8_t* const aq = p.a_q + (int64_t)row0 * arow;
+  const uint8_t* const as = p.a_s + (int64_t)row0 * srow;
+  const uint8_t* const wq = p.w_q + ((int64_t)t.expert * N + n0) * wrow;
+  const uint8_t* const ws = p.w_s + ((int64_t)t.expert * N + n0) * srow;
+
+  // rows past the tile's repeat the last and are never stored
+  uint32_t offA[S::NA], offW[S::NW];
+#pragma unroll
+  for (int u = 0; u < S::NA; ++u) {
+    if constexpr (A8) {
+      const int r = (wv * S::NA + u) * 8 + (lane >> 3);
+      offA[u] = min(r, rows - 1) * arow + 16 * ((lane & 7) ^ (r & 7));
+    } else {
+      const int r = (wv * S::NA + u) * 16 + (lane >> 2);
+      offA[u] = min(r, rows - 1) * arow + 16 * ((lane & 3) ^ ((r >> 1) & 3));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < S::NW; ++u) {
+    const int r = (wv * S::NW + u) * 16 + (lane >> 2);
+    offW[u] = min(r, feats - 1) * wrow + 16 * ((lane & 3) ^ ((r >> 1) & 3));
+  }
+  const uint32_t lds0 = (uint32_t)(size_t)(lds_void_t*)mg_lds;
+  // rows 16 b .. +15 (A's, then W's) of scale group gr (stages 4 gr .. +3; past the last: the last's)
+  auto issue_scales = [&](int gr, int b) {
+    b = min(b, S::ROWS / 16 - 1);
+    const int r = 16 * b + (lane >> 2);
+    const uint32_t k = 4 * min(4 * gr + (lane & 3), nk - 1);
+    const uint32_t dst = lds0 + S::SC + (uint32_t)(gr % 3) * (S::ROWS * 16) + 256 * b;
+    if (16 * b < BM) dma4(as, min(r, rows - 1) * srow + k, dst);
+    else dma4(ws, min(r - BM, feats - 1) * srow + k, dst);
+  };
+  auto issue_stage = [&](int kt) {
+    const uint32_t st = lds0 + (uint32_t)(kt % NS) * S::STAGE;
+    const uint8_t* const ab = aq + kt * (A8 ? 128 : 64);
+    const uint8_t* const wb = wq + kt * 64;
+#pragma unroll
+    for (int u = 0; u < S::NA; ++u) dma16(ab, offA[u], st + (wv * S::NA + u) * 1024);
+#pragma unroll
+    for (int u = 0; u < S::NW; ++u) dma16(wb, offW[u], st + S::A + (wv * S::NW + u) * 1024);
+#pragma unroll
+    for (int s = 0; s < S::SL; ++s) issue_scales((kt >> 2) + 1, ((kt & 3) * 4 + wv) * S::SL + s);
+  };
+
+  mg_int8 fa[S::TM][2];
+  mg_int4 fw[S::TN][2];
+  uint32_t sa[S::TM], sw[S::TN];
+  float16v acc[S::TM][S::TN];
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  auto read_stage = [&](int kt) {
+    const uint8_t* const st = mg_lds + (kt % NS) * S::STAGE;
+    const uint8_t* const sc = mg_lds + S::SC + (kt >> 2) % 3 * (S::ROWS * 16) + 4 * (kt & 3);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+      const int row = wm * (BM / 2) + 32 * i + r32;
+      sa[i] = *reinterpret_cast<const uint32_t*>(sc + 16 * row) >> (8 * h);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if constexpr (A8) {
+          const mg_int4 lo = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, 4 * s + h));
+          const mg_int4 hi = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, 4 * s + 2 + h));
+          fa[i][s] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+          const mg_int4 v = *reinterpret_cast<const mg_int4*>(st + fp4_quad_off(row, 2 * s + h));
+          fa[i][s] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) {
+      const int row = wn * (BN / 2) + 32 * j + r32;
+      sw[j] = *reinterpret_cast<const uint32_t*>(sc + 16 * (BM + row)) >> (8 * h);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fw[j][s] = *reinterpret_cast<const mg_int4*>(st + S::A + fp4_quad_off(row, 2 * s + h));
+    }
+  };
+  // D = W A^T: lane = one row of A, groups of four consecutive features
+  auto multiply = [&]() {
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            __builtin_shufflevector(fw[j][0], fw[j][0], 0, 1, 2, 3, -1, -1, -1, -1), fa[i][0], acc[i][j], 4, A8 ? 0 : 4, 0,
+            (int)sw[j], 0, (int)sa[i]);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            __builtin_shufflevector(fw[j][1], fw[j][1], 0, 1, 2, 3, -1, -1, -1, -1), fa[i][1], acc[i][j], 4, A8 ? 0 : 4, 2,
+            (int)sw[j], 2, (int)sa[i]);
+  };
+
+  for (int s = 0; s < 4 * S::SL; ++s) issue_scales(0, wv * 4 * S::SL + s);
+  constexpr int AHEAD = NS == 2 ? 2 : NS - 1;   // stages in flight at a stage's wait
+#pragma unroll
+  for (int s = 0; s < AHEAD; ++s)
+    if (s < nk) issue_stage(s);
+  for (int kt = 0; kt < nk; ++kt) {
+    // stage kt has landed when only the AHEAD - 1 after it are in flight
+    if (nk - kt >= AHEAD) wait_vm<S::LPS * (AHEAD - 1)>();
+    else wait_vm<0>();
+    wait_lgkm_barrier();
+    if constexpr (NS > 2) {
+      if (kt + AHEAD < nk) issue_stage(kt + AHEAD);
+      read_stage(kt);
+    } else {
+      read_stage(kt);
+      wait_lgkm_barrier();
+      if (kt + AHEAD < nk) issue_stage(kt + AHEAD);
+    }
+    multiply();
+  }
+
+  // epilogue: block (i, j), register e of lane l: row 32 i + l % 32, feature
+  // 32 j + 8 (e / 4) + 4 (l / 32) + e % 4 of the wavefront's part
+  const int mrow = row0 + wm * (BM / 2), mleft = rows - wm * (BM / 2);
+  const int ncol = n0 + wn * (BN / 2), nleft = feats - wn * (BN / 2);
+  const float* const bias = p.bias ? p.bias + (int64_t)t.expert * N + n0 : nullptr;
+  auto biased = [&](int i, int j, int q, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = acc[i][j][4 * q + e];
+      if (bias) v[e] = v[e] + bias[min(wn * (BN / 2) + 32 * j + 8 * q + 4 * h + e, feats - 1)];
+    }
+  };
+  if (p.out_f32) {
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+          biased(i, j, q, v);
+          const int r = 32 * i + r32, c = 32 * j + 8 * q + 4 * h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r < mleft && c + e < nleft) static_cast<float*>(p.y)[(int64_t)(mrow + r) * p.ldy + ncol + c + e] = v[e];
+        }
+    return;
+  }
+  // bf16: through LDS, so that a row's features leave in whole 16-byte pieces
+  wait_lgkm_barrier();                          // all are done with the ring
+  uint8_t* const out = mg_lds + wv * (BM / 2) * S::OUTROW;
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+        biased(i, j, q, v);
+        *reinterpret_cast<uint2*>(out + (32 * i + r32) * S::OUTROW + 2 * (32 * j + 8 * q + 4 * h)) =
+            make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+      }
+  // the wavefront reads back what it wrote (its LDS operations run in order)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  constexpr int PPR = BN / 16;                  // 16-byte pieces of a row
+  const bool whole = N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
+#pragma unroll
+  for (int it = 0; it < (BM / 2) * PPR / 64; ++it) {
+    const int r = it * (64 / PPR) + lane / PPR, c = 8 * (lane % PPR);
+    const uint4 v = *reinterpret_cast<const uint4*>(out + r * S::OUTROW + 2 * c);
+    if (r >= mleft || c >= nleft) continue;
+    uint16_t* const y = static_cast<uint16_t*>(p.y) + (int64_t)(mrow + r) * p.ldy + ncol + c;
+    if (whole) {
+      *reinterpret_cast<uint4*>(y) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < nleft) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+template <bool A8, int BM, int BN, int NS>
+static hipError_t launch_tile(const MxGrouped& q, hipStream_t st) {
+  using S = MgTile<A8, BM, BN, NS>;
+  const hipError_t e = allow_lds_once<(A8 * 8 + NS) * (1 << 20) + BM * 1024 + BN>(reinterpret_cast<const void*>(&mx_tile_kernel<A8, BM, BN, NS>), S::LDS);
+  if (e != hipSuccess) return e;
+  const int64_t grid = (int64_t)(q.T / BM + q.E) * ((q.N + BN - 1) / BN);
+  hipLaunchKernelGGL((mx_tile_kernel<A8, BM, BN, NS>), dim3((unsigned)grid), dim3(256), S::LDS, st, q);
+  return hipGetLastError();
 }
 
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st) {
   // fp32 output of MXFP8 rows: sums of exact products (the block-scaled
   // instruction cuts small products of E4M3 operands)
   if (a_fp8 && q.out_f32) return launch_qgemm_mx_grouped_exact(a_fp8, q, st);
-  const char* tv = getenv("BIG");
-  if (q.T / q.E >= (tv ? atoi(tv) : 64)) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
-  if (q.K > 2 * kMgMaxWaves * kMgStep) return launch_qgemm_mx_grouped_exact(a_fp8, q, st);
-  return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
+  // By the average rows of an expert (their counts are on the device), both
+  // sides of each border measured with skewed counts, MXFP8, us:
+  //   N x K x experts     8 rows            16                32       128              256
+  //   1920 x 3072 x 16    stream 16, 64: 19 stream 20, 64: 19 28, 19   64: 31, 256: 44  64: 49, 256: 46
+  //   7680 x 1920 x 8     17, 19            20, 19            23, 19   36, 38           69, 69
+  //   3072 x 12288 x 8    41, 57            55, 57            80, 60   88, 150          -
+  const int avg = q.T / q.E;
+  if (avg >= 192) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
+  if (avg <= 12 && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
+  // three stages where three workgroups still fit a compute unit
+  return a_fp8 ? launch_tile<true, 64, 128, 2>(q, st) : launch_tile<false, 64, 128, 3>(q, st);
 }
 
 }  // namespace vdtq

@@ -13,6 +13,7 @@ namespace vdtq {
 
 struct RowTile {
   int expert, row0, rows;      // first row, and the expert's rows from there on (0: no such tile)
+  int before, tiles;           // tiles of the experts before this one, and its own
 };
 
 // Running maximum and sum over the 64 lanes.
@@ -66,22 +67,25 @@ __device__ __forceinline__ int row_tiles(const int32_t* offsets, int E, int T, i
 
 // Tile t (0 <= t < row_tiles).
 __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int E, int T, int bm, int t) {
-  RowTile r{0, 0, 0};
+  RowTile r{0, 0, 0, 0, 0};
+  int past = 0;                                         // tiles of the 64s before
   each_group(offsets, E, T, bm, [&](int e0, int lo, int hi, int upto) {
     const int all = __shfl(upto, 63, 64);
-    if (t >= all) {
-      t -= all;
+    if (t >= past + all) {
+      past += all;
       return false;
     }
-    const int i = __builtin_ctzll(__ballot(upto > t));   // the first lane whose tiles reach past t
-    const int before = i ? __shfl(upto, i - 1, 64) : 0;
+    const int i = __builtin_ctzll(__ballot(past + upto > t));   // the first lane whose tiles reach past t
+    const int before = past + (i ? __shfl(upto, i - 1, 64) : 0);
     const int row0 = __shfl(lo, i, 64) + (t - before) * bm;
-    r = RowTile{e0 + i, row0, __shfl(hi, i, 64) - row0};
+    r = RowTile{e0 + i, row0, __shfl(hi, i, 64) - row0, before, past + __shfl(upto, i, 64) - before};
     return true;
   });
   r.expert = __builtin_amdgcn_readfirstlane(r.expert);
   r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
   r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+  r.before = __builtin_amdgcn_readfirstlane(r.before);
+  r.tiles = __builtin_amdgcn_readfirstlane(r.tiles);
   return r;
 }
 
