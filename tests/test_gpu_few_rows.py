@@ -296,17 +296,22 @@ def test_grouped_rows_that_are_not_finite():
 
 
 def test_grouped_equal_experts_are_one_product():
-    """Rows in two groups of the same weights give the bits of one group."""
+    """Rows in two groups of the same weights give the bits of one group
+    where both calls take the same kernel, and sums of another order (twice
+    the bound of one) where 24 rows of one expert and 12 of each of two do
+    not."""
     need_gpu()
     rng = rng_of(25)
-    for T, cut in ((24, 9), (600, 256)):
+    for T, cut, same in ((12, 5, True), (24, 9, False), (600, 256, True)):
         N, K = 128, 512
-        _, ad = acts(rng, T, K, "mxfp8")
+        (aq, as_), ad = acts(rng, T, K, "mxfp8")
         (q, s), one = weights(rng, N, K, "mx")
         two = V.MXTensor(dev(np.concatenate([q, q])), dev(np.concatenate([s, s])), "mxfp4")
         a = V.qgemm_mx_grouped(ad, one, dev(np.array([0, T], np.int32)), None, "f32")
         b = V.qgemm_mx_grouped(ad, two, dev(np.array([0, cut, T], np.int32)), None, "f32")
-        assert torch.equal(a, b)
+        if same:
+            assert torch.equal(a, b)
+        assert_elementwise(values(a), values(b), 2 * terms_mx(aq, as_, "mxfp8", q, s, None), K, "f32")
 
 
 # -------------------------------------------------------- the run together

@@ -89,8 +89,9 @@ static hipError_t allow_lds_once(const void* kernel, int bytes) {
 }
 
 // Rows grouped by expert (MX operands): the choice of a kernel
-// (qgemm_mx_grouped.hip) and the ones it chooses between: 256 x 256 tiles
-// (qgemm_mx.hip) and sums of exact products (qgemv.hip).
+// (qgemm_mx_grouped.hip) and the ones of other files it chooses between:
+// 256 x 256 tiles (qgemm_mx.hip), and sums of exact products of few MXFP8
+// rows (qgemv.hip).
 struct MxGrouped {
   const uint8_t *a_q, *a_s, *w_q, *w_s;
   const float* bias;             // [E][N] or NULL
@@ -102,7 +103,7 @@ struct MxGrouped {
 };
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st);
 hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const MxGrouped& q, hipStream_t st);
-hipError_t launch_qgemm_mx_grouped_exact(bool a_fp8, const MxGrouped& q, hipStream_t st);
+hipError_t launch_qgemm_mx_grouped_exact(const MxGrouped& q, hipStream_t st);
 
 size_t bs_workspace_bytes(int64_t n);
 hipError_t launch_block_stats(const void* in, const void* out, const void* dprev, void* dnew,

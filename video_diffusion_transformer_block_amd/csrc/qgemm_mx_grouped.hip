@@ -193,6 +193,13 @@ static hipError_t stream(const MxGrouped& q, hipStream_t st) {
   return launch_stream<A8, 2>(q, (steps + 1) / 2, st);
 }
 
+typedef __bf16 mg_bf16x8 __attribute__((ext_vector_type(8)));
+template <class P>
+__device__ __forceinline__ mg_bf16x8 join8(P a, P b, P c, P d) {
+  return __builtin_bit_cast(mg_bf16x8, make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                  __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)));
+}
+
 // ------------------------------------------------------ tiles of BM x BN
 // Experts of middling row counts.  A workgroup of 4 wavefronts (2 x 2) owns
 // BM rows of one expert times BN features, several workgroups share a compute
@@ -223,7 +230,12 @@ struct MgTile {
   static constexpr int WGS = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;   // workgroups of a compute unit
 };
 
-template <bool A8, int BM, int BN, int NS, int WGS = MgTile<A8, BM, BN, NS>::WGS>
+//
+// EXACT (MXFP8 rows, fp32 output): the fragments are decoded to bf16 (every
+// element times its block's power of two is exact) for
+// v_mfma_f32_32x32x16_bf16, which does not cut products against each other.
+// A lane then holds whole blocks of 32: step s, half l / 32: block 2 s + l / 32.
+template <bool A8, int BM, int BN, int NS, bool EXACT = false, int WGS = MgTile<A8, BM, BN, NS>::WGS>
 __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   using S = MgTile<A8, BM, BN, NS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t mg_lds[];
@@ -313,8 +325,8 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if constexpr (A8) {
-          const mg_int4 lo = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, 4 * s + h));
-          const mg_int4 hi = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, 4 * s + 2 + h));
+          const mg_int4 lo = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, EXACT ? 4 * s + 2 * h : 4 * s + h));
+          const mg_int4 hi = *reinterpret_cast<const mg_int4*>(st + i8_quad_off(row, EXACT ? 4 * s + 2 * h + 1 : 4 * s + 2 + h));
           fa[i][s] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
           const mg_int4 v = *reinterpret_cast<const mg_int4*>(st + fp4_quad_off(row, 2 * s + h));
@@ -332,6 +344,33 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   };
   // D = W A^T: lane = one row of A, groups of four consecutive features
   auto multiply = [&]() {
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {           // 8 of the block's 32 elements
+          mg_bf16x8 a[S::TM], w[S::TN];
+#pragma unroll
+          for (int i = 0; i < S::TM; ++i) {
+            const float sc = __uint_as_float((sa[i] >> (16 * s) & 0xFFu) << 23);
+            const uint32_t lo = (uint32_t)fa[i][s][2 * k], hi = (uint32_t)fa[i][s][2 * k + 1];
+            a[i] = join8(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, true),
+                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, sc, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, sc, true));
+          }
+#pragma unroll
+          for (int j = 0; j < S::TN; ++j) {
+            const float sc = __uint_as_float((sw[j] >> (16 * s) & 0xFFu) << 23);
+            const uint32_t c = (uint32_t)fw[j][s][k];
+            w[j] = join8(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 0), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 1),
+                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 2), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, sc, 3));
+          }
+#pragma unroll
+          for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], a[i], acc[i][j], 0, 0, 0);
+        }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < S::TM; ++i)
 #pragma unroll
@@ -382,6 +421,7 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
     }
   };
   if (p.out_f32) {
+    const bool whole4 = N % 4 == 0 && p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
 #pragma unroll
     for (int i = 0; i < S::TM; ++i)
 #pragma unroll
@@ -391,9 +431,15 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
           float v[4];
           biased(i, j, q, v);
           const int r = 32 * i + r32, c = 32 * j + 8 * q + 4 * h;
+          if (r >= mleft) continue;
+          float* const y = static_cast<float*>(p.y) + (int64_t)(mrow + r) * p.ldy + ncol + c;
+          if (whole4 && c < nleft) {
+            *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r < mleft && c + e < nleft) static_cast<float*>(p.y)[(int64_t)(mrow + r) * p.ldy + ncol + c + e] = v[e];
+            for (int e = 0; e < 4; ++e)
+              if (c + e < nleft) y[e] = v[e];
+          }
         }
     return;
   }
@@ -433,20 +479,18 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   }
 }
 
-template <bool A8, int BM, int BN, int NS>
+template <bool A8, int BM, int BN, int NS, bool EXACT = false>
 static hipError_t launch_tile(const MxGrouped& q, hipStream_t st) {
   using S = MgTile<A8, BM, BN, NS>;
-  const hipError_t e = allow_lds_once<(A8 * 8 + NS) * (1 << 20) + BM * 1024 + BN>(reinterpret_cast<const void*>(&mx_tile_kernel<A8, BM, BN, NS>), S::LDS);
+  const hipError_t e = allow_lds_once<(EXACT * 16 + A8 * 8 + NS) * (1 << 20) + BM * 1024 + BN>(
+      reinterpret_cast<const void*>(&mx_tile_kernel<A8, BM, BN, NS, EXACT>), S::LDS);
   if (e != hipSuccess) return e;
   const int64_t grid = (int64_t)(q.T / BM + q.E) * ((q.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx_tile_kernel<A8, BM, BN, NS>), dim3((unsigned)grid), dim3(256), S::LDS, st, q);
+  hipLaunchKernelGGL((mx_tile_kernel<A8, BM, BN, NS, EXACT>), dim3((unsigned)grid), dim3(256), S::LDS, st, q);
   return hipGetLastError();
 }
 
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st) {
-  // fp32 output of MXFP8 rows: sums of exact products (the block-scaled
-  // instruction cuts small products of E4M3 operands)
-  if (a_fp8 && q.out_f32) return launch_qgemm_mx_grouped_exact(a_fp8, q, st);
   // By the average rows of an expert (their counts are on the device), both
   // sides of each border measured with skewed counts, MXFP8, us:
   //   N x K x experts     8 rows            16                32       128              256
@@ -454,6 +498,15 @@ hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t s
   //   7680 x 1920 x 8     17, 19            20, 19            23, 19   36, 38           69, 69
   //   3072 x 12288 x 8    41, 57            55, 57            80, 60   88, 150          -
   const int avg = q.T / q.E;
+  // fp32 output of MXFP8 rows: sums of exact products, which the block-scaled
+  // instruction does not form.  8 rows an expert: 17 us by the few-row kernel,
+  // 27 by tiles (1920 x 3072 x 16), 58 and 78 (3072 x 12288 x 8); 16 rows: 28
+  // and 27, 87 and 80; tiles of 128 x 128 are 8 % faster at thousands of rows,
+  // 40 % slower below 64
+  if (a_fp8 && q.out_f32) {
+    if (avg <= 12) return launch_qgemm_mx_grouped_exact(q, st);
+    return launch_tile<true, 64, 128, 2, true>(q, st);
+  }
   if (avg >= 192) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
   if (avg <= 12 && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
   // three stages where three workgroups still fit a compute unit

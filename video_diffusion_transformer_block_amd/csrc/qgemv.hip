@@ -436,19 +436,14 @@ hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t
   }
 }
 
-hipError_t launch_qgemm_mx_grouped_exact(bool a_fp8, const MxGrouped& q, hipStream_t st) {
+hipError_t launch_qgemm_mx_grouped_exact(const MxGrouped& q, hipStream_t st) {
   GemvParams p{};
   p.a_q = q.a_q; p.a_s = q.a_s;
   p.w_q = q.w_q; p.w_s = q.w_s; p.bias = q.bias; p.offsets = q.offsets;
   p.y = q.y; p.ldy = q.ldy; p.out_f32 = q.out_f32;
   p.M = q.T; p.N = q.N; p.K = q.K; p.E = q.E;
   // 4 feature tiles a workgroup: finding its rows takes about as long as one
-  if (q.T / q.E <= 8) {
-    const int gy = q.T / 16 + q.E;
-    return a_fp8 ? launch_tiles<kActMx8, 16>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 16>(p, gy, 4, kGvMaxLds / 2, st);
-  }
-  const int gy = q.T / 32 + q.E;
-  return a_fp8 ? launch_tiles<kActMx8, 32>(p, gy, 4, kGvMaxLds / 2, st) : launch_tiles<kActMx4, 32>(p, gy, 4, kGvMaxLds / 2, st);
+  return launch_tiles<kActMx8, 16>(p, q.T / 16 + q.E, 4, kGvMaxLds / 2, st);
 }
 
 }  // namespace vdtq
