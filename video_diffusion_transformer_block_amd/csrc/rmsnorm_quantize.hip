@@ -39,17 +39,37 @@ struct RnParams {
   uint8_t* q;
   void* scales;
   int64_t ldx, ldr, lds;
-  float eps, had_scale;     // RN(1 / sqrt(had_block))
+  float eps;
+  float had_scale;          // RN(1 / sqrt(had_block)) when that is no power of two, else 1
+  int32_t had_shift;        // otherwise 1 / sqrt(had_block) = 2^-had_shift
   int32_t M, K, b;
 };
+
+// The value of lane l ^ O (O < 32: within a row of 32 lanes at most), by data
+// movement inside the vector unit where there is one: a shuffle through the
+// LDS crossbar per butterfly made the pass 12 us slower (88 us, 17776 x 3072).
+template <int O>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);          // quads 1 0 3 2
+  else if constexpr (O == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);     // quads 2 3 0 1
+  else if constexpr (O == 4)                                                               // l ^ 7, then ^ 3
+    return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
+  else if constexpr (O == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xF, 0xF, true);    // rows of 16 turned by 8
+  else return __shfl_xor(v, O, 64);
+}
+template <int O>
+__device__ __forceinline__ float lane_xor(float v) { return __uint_as_float(lane_xor<O>(__float_as_uint(v))); }
+template <int O>
+__device__ __forceinline__ double lane_xor(double v) {
+  return u2d(lane_xor<O>((uint32_t)__double2loint(v)), lane_xor<O>((uint32_t)__double2hiint(v)));
+}
 
 // Sum and maximum over the T lanes of a row; for T = 256 through LDS (one
 // slot per wavefront; each use has slots of its own).
 template <int T>
 __device__ __forceinline__ double row_sum(double v, double* slot) {
-  constexpr int W = T < 64 ? T : 64;
-#pragma unroll
-  for (int o = W / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  v += lane_xor<1>(v); v += lane_xor<2>(v); v += lane_xor<4>(v); v += lane_xor<8>(v);
+  if constexpr (T >= 64) { v += lane_xor<16>(v); v += lane_xor<32>(v); }
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -61,9 +81,8 @@ __device__ __forceinline__ double row_sum(double v, double* slot) {
 }
 template <int T>
 __device__ __forceinline__ float row_max(float v, float* slot) {
-  constexpr int W = T < 64 ? T : 64;
-#pragma unroll
-  for (int o = W / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  v = fmaxf(v, lane_xor<1>(v)); v = fmaxf(v, lane_xor<2>(v)); v = fmaxf(v, lane_xor<4>(v)); v = fmaxf(v, lane_xor<8>(v));
+  if constexpr (T >= 64) { v = fmaxf(v, lane_xor<16>(v)); v = fmaxf(v, lane_xor<32>(v)); }
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -87,8 +106,18 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(rn_pair(v[0], v[1]), rn_pair(v[2], v[3]), rn_pair(v[4], v[5]), rn_pair(v[6], v[7]));
 }
 
+// One butterfly stage between lanes l and l ^ O: the lower lane keeps the
+// sum, the upper the difference (other - own); -v is exact.
+template <int O>
+__device__ __forceinline__ void butterfly(float (&v)[8]) {
+  const uint32_t flip = threadIdx.x & O ? 0x80000000u : 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = lane_xor<O>(v[i]) + __uint_as_float(__float_as_uint(v[i]) ^ flip);
+}
+
 // Butterflies of one vector of 8 per lane, blocks of b elements (b / 8
-// lanes), in the order h = 1, 2, ..., b / 2; then the normalisation.
+// lanes), in the order h = 1, 2, ..., b / 2; then the normalisation unless
+// that is a power of two, which the callers fold into their scales.
 __device__ __forceinline__ void fwht8(float (&v)[8], int b, float scale) {
 #pragma unroll
   for (int h = 1; h < 8; h <<= 1)
@@ -99,16 +128,15 @@ __device__ __forceinline__ void fwht8(float (&v)[8], int b, float scale) {
         v[i] = a + c;
         v[i + h] = a - c;
       }
-  for (int o = 1; o < b / 8; o <<= 1) {
-    const bool upper = threadIdx.x & o;
+  butterfly<1>(v);
+  if (b >= 32) butterfly<2>(v);
+  if (b >= 64) butterfly<4>(v);
+  if (b >= 128) butterfly<8>(v);
+  if (b >= 256) butterfly<16>(v);
+  if (scale != 1.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_xor(v[i], o, 64);
-      v[i] = upper ? (other - v[i]) : (v[i] + other);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * scale;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = v[i] * scale;
 }
 
 template <int T, int C, int FMT>
@@ -192,15 +220,17 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * T + t;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[c][e] = __builtin_ldexpf(y[c][e], -p.had_shift);
       uint4 w = pack8(y[c]);
       if (!finite) w = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
       if (live && i < nv) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.q) + row * p.K + 8 * i) = w;
     }
   } else if constexpr (FMT == VDTQ_FMT_INT8) {
-    const float a = row_max<T>(av, max_slot);
+    const float a = __builtin_ldexpf(row_max<T>(av, max_slot), -p.had_shift);
     const bool ok = finite && a >= kZeroLimit && a <= 3.0e38f;
     const float s = ok ? a / 127.0f : (finite && a < kZeroLimit ? 0.0f : __builtin_nanf(""));
-    const float qi = ok ? 1.0f / s : 0.0f;
+    const float qi = __builtin_ldexpf(ok ? 1.0f / s : 0.0f, -p.had_shift);
     // rint_even(y * qi): the low byte of RN(y * qi) + 1.5 * 2^23 is the code
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -225,15 +255,12 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
       float a = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(y[c][e]));
-      a = fmaxf(a, __shfl_xor(a, 1, 64));
-      a = fmaxf(a, __shfl_xor(a, 2, 64));
-      const int ex = mx_exponent<FP8 ? 8 : 2, 0>(a);
-      // y * 2^-ex as two exact factors, each a normal fp32
-      const int n1 = ex / 2, n2 = ex - n1;
-      const float m1 = exp2i(-n1), m2 = exp2i(-n2);
+      a = fmaxf(a, lane_xor<1>(a));
+      a = fmaxf(a, lane_xor<2>(a));
+      const int ex = mx_exponent<FP8 ? 8 : 2, 0>(__builtin_ldexpf(a, -p.had_shift));
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (y[c][e] * m1) * m2;
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(y[c][e], -ex - p.had_shift);
       const bool st = live && i < nv;
       if constexpr (FP8) {
         uint32_t w[2];
@@ -286,9 +313,17 @@ hipError_t launch_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t 
   p.scales = scales;
   p.ldx = ldx; p.ldr = ldr; p.lds = lds;
   p.eps = eps;
-  p.had_scale = b == 16 ? HadScale<16>::f : b == 32 ? HadScale<32>::f : b == 64 ? HadScale<64>::f
-                : b == 128 ? HadScale<128>::f : HadScale<256>::f;
+  p.had_shift = b == 16 ? 2 : b == 64 ? 3 : b == 256 ? 4 : 0;
+  p.had_scale = b == 32 ? HadScale<32>::f : b == 128 ? HadScale<128>::f : 1.0f;
   p.M = (int32_t)M; p.K = (int32_t)K; p.b = b;
+  const char* tv = getenv("ROWS");
+  const int v = tv ? atoi(tv) : 0;
+  if (v == 1) {
+    if (K <= 1024) return launch_fmt<64, 2>(p, fmt, st);
+    if (K <= 2048) return launch_fmt<64, 4>(p, fmt, st);
+    if (K <= 3072) return launch_fmt<64, 6>(p, fmt, st);
+    if (K <= 4096) return launch_fmt<64, 8>(p, fmt, st);
+  }
   if (K <= 2048) return launch_fmt<256, 1>(p, fmt, st);
   if (K <= 4096) return launch_fmt<256, 2>(p, fmt, st);
   if (K <= 8192) return launch_fmt<256, 4>(p, fmt, st);
