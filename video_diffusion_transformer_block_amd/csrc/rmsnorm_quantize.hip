@@ -13,8 +13,12 @@
 // registers: the pass reads x and the residual once and writes the stream
 // and the codes once.
 //
-// Layout: T lanes own a row (T = 16, 64 or 256), each holding C vectors of
-// 8 consecutive elements, vector c of lane t at element 8 (c T + t): every
+// Bound: memory.  17776 x 3072 with residual, MXFP8 out, moves 384 MB in 70.6
+// us (5.4 TB/s; a plain copy of 1 GB reaches 5.2 on the same card); the vector
+// unit is busy for about 40 us of it.
+//
+// Layout: T lanes own a row (T = 8, 16, 64, 128 or 256), each holding C vectors
+// of 8 consecutive elements, vector c of lane t at element 8 (c T + t): every
 // load and store of a wavefront is one contiguous run.  The butterflies
 // h = 1, 2, 4 stay in a lane, h = 8 .. 128 pair lanes t and t ^ (h / 8);
 // an MX block is four neighbouring lanes.
@@ -46,8 +50,9 @@ struct RnParams {
 };
 
 // The value of lane l ^ O (O < 32: within a row of 32 lanes at most), by data
-// movement inside the vector unit where there is one: a shuffle through the
-// LDS crossbar per butterfly made the pass 12 us slower (88 us, 17776 x 3072).
+// movement inside the vector unit where there is one: a shuffle through
+// the LDS crossbar for each butterfly made the pass 8 us slower (88 us, 17776 x
+// 3072).
 template <int O>
 __device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
   if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);          // quads 1 0 3 2
@@ -64,11 +69,12 @@ __device__ __forceinline__ double lane_xor(double v) {
   return u2d(lane_xor<O>((uint32_t)__double2loint(v)), lane_xor<O>((uint32_t)__double2hiint(v)));
 }
 
-// Sum and maximum over the T lanes of a row; for T = 256 through LDS (one
-// slot per wavefront; each use has slots of its own).
+// Sum and maximum over the T lanes of a row; for T = 128 and 256 through LDS
+// (one slot per wavefront; each use has slots of its own).
 template <int T>
 __device__ __forceinline__ double row_sum(double v, double* slot) {
-  v += lane_xor<1>(v); v += lane_xor<2>(v); v += lane_xor<4>(v); v += lane_xor<8>(v);
+  v += lane_xor<1>(v); v += lane_xor<2>(v); v += lane_xor<4>(v);
+  if constexpr (T >= 16) v += lane_xor<8>(v);
   if constexpr (T >= 64) { v += lane_xor<16>(v); v += lane_xor<32>(v); }
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
@@ -81,7 +87,8 @@ __device__ __forceinline__ double row_sum(double v, double* slot) {
 }
 template <int T>
 __device__ __forceinline__ float row_max(float v, float* slot) {
-  v = fmaxf(v, lane_xor<1>(v)); v = fmaxf(v, lane_xor<2>(v)); v = fmaxf(v, lane_xor<4>(v)); v = fmaxf(v, lane_xor<8>(v));
+  v = fmaxf(v, lane_xor<1>(v)); v = fmaxf(v, lane_xor<2>(v)); v = fmaxf(v, lane_xor<4>(v));
+  if constexpr (T >= 16) v = fmaxf(v, lane_xor<8>(v));
   if constexpr (T >= 64) { v = fmaxf(v, lane_xor<16>(v)); v = fmaxf(v, lane_xor<32>(v)); }
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
@@ -139,9 +146,29 @@ __device__ __forceinline__ void fwht8(float (&v)[8], int b, float scale) {
   }
 }
 
-template <int T, int C, int FMT>
-__global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
-  constexpr int ROWS = 256 / T;                     // rows per workgroup
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+// The outputs are written once and leave for memory at once (non-temporal:
+// 15.3 -> 14.1 us for 4446 x 1920, 79 -> 76 us for 17776 x 3072).
+__device__ __forceinline__ void store16(void* p, uint4 w) {
+  __builtin_nontemporal_store(uint4v{w.x, w.y, w.z, w.w}, static_cast<uint4v*>(p));
+}
+__device__ __forceinline__ void store8(void* p, uint2 w) {
+  __builtin_nontemporal_store(uint2v{w.x, w.y}, static_cast<uint2v*>(p));
+}
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  const uint4v* q = static_cast<const uint4v*>(p);
+  const uint4v v = NT ? __builtin_nontemporal_load(q) : *q;
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Threads of a workgroup of T-lane rows.
+constexpr int rn_threads(int T) { return T == 128 ? 128 : 256; }
+
+// NTL: the inputs are read past the caches (below).
+template <int T, int C, int FMT, bool NTL>
+__global__ __launch_bounds__(rn_threads(T)) void rmsnorm_quantize_kernel(RnParams p) {
+  constexpr int ROWS = rn_threads(T) / T;           // rows per workgroup
   __shared__ double sum_slot[4];
   __shared__ float max_slot[4];
   const int t = threadIdx.x % T;
@@ -154,7 +181,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
   for (int c = 0; c < C; ++c) {
     const int i = c * T + t;
     r[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && i < nv) r[c] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + 8 * i);
+    if (live && i < nv) r[c] = load16<NTL>(p.x + row * p.ldx + 8 * i);
   }
   if (p.res) {
     uint4 s[C];
@@ -162,7 +189,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
     for (int c = 0; c < C; ++c) {
       const int i = c * T + t;
       s[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && i < nv) s[c] = *reinterpret_cast<const uint4*>(p.res + row * p.ldr + 8 * i);
+      if (live && i < nv) s[c] = load16<NTL>(p.res + row * p.ldr + 8 * i);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -189,7 +216,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * T + t;
-      if (live && i < nv) *reinterpret_cast<uint4*>(p.sum + row * p.lds + 8 * i) = r[c];
+      if (live && i < nv) store16(p.sum + row * p.lds + 8 * i, r[c]);
     }
   }
   const bool finite = ss < __builtin_inf();         // false for NaN too
@@ -224,7 +251,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
       for (int e = 0; e < 8; ++e) y[c][e] = __builtin_ldexpf(y[c][e], -p.had_shift);
       uint4 w = pack8(y[c]);
       if (!finite) w = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-      if (live && i < nv) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.q) + row * p.K + 8 * i) = w;
+      if (live && i < nv) store16(reinterpret_cast<uint16_t*>(p.q) + row * p.K + 8 * i, w);
     }
   } else if constexpr (FMT == VDTQ_FMT_INT8) {
     const float a = __builtin_ldexpf(row_max<T>(av, max_slot), -p.had_shift);
@@ -244,7 +271,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
         const uint32_t b3 = __float_as_uint(y[c][4 * h + 3] * qi + 12582912.0f);
         w[h] = ok ? (__builtin_amdgcn_perm(b1, b0, 0x0c0c0400u) | (__builtin_amdgcn_perm(b3, b2, 0x0c0c0400u) << 16)) : 0u;
       }
-      if (live && i < nv) *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * i) = make_uint2(w[0], w[1]);
+      if (live && i < nv) store8(p.q + row * p.K + 8 * i, make_uint2(w[0], w[1]));
     }
     if (live && t == 0) static_cast<float*>(p.scales)[row] = s;
   } else {
@@ -273,7 +300,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
           x = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], x, true);
           w[h] = finite ? (uint32_t)x : 0u;
         }
-        if (st) *reinterpret_cast<uint2*>(p.q + row * p.K + 8 * i) = make_uint2(w[0], w[1]);
+        if (st) store8(p.q + row * p.K + 8 * i, make_uint2(w[0], w[1]));
       } else {
         uint32_t x = 0u;
         x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(x, v[0], v[1], 1.0f, 0);
@@ -288,16 +315,42 @@ __global__ __launch_bounds__(256) void rmsnorm_quantize_kernel(RnParams p) {
   }
 }
 
-template <int T, int C>
+template <int T, int C, bool NTL>
 static hipError_t launch_fmt(const RnParams& p, int fmt, hipStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)p.M + 256 / T - 1) / (256 / T))), block(256);
+  constexpr int B = rn_threads(T), ROWS = B / T;
+  const dim3 grid((unsigned)(((int64_t)p.M + ROWS - 1) / ROWS)), block(B);
   switch (fmt) {
-    case VDTQ_FMT_INT8: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_INT8>), grid, block, 0, st, p); break;
-    case VDTQ_FMT_BF16: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_BF16>), grid, block, 0, st, p); break;
-    case VDTQ_FMT_MXFP4: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP4>), grid, block, 0, st, p); break;
-    default: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP8>), grid, block, 0, st, p); break;
+    case VDTQ_FMT_INT8: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_INT8, NTL>), grid, block, 0, st, p); break;
+    case VDTQ_FMT_BF16: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_BF16, NTL>), grid, block, 0, st, p); break;
+    case VDTQ_FMT_MXFP4: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP4, NTL>), grid, block, 0, st, p); break;
+    default: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP8, NTL>), grid, block, 0, st, p); break;
   }
   return hipGetLastError();
+}
+
+// Lanes and vectors of a row: the fewest lanes that hold it in a few vectors
+// each.  Few lanes leave more rows to a workgroup (512 columns: 75 us for
+// 100000 rows with 64 lanes, 162 with 256; 64 columns: 103 us for 800000 rows
+// with 16 lanes, 1040 with 256); from 1025 columns on 256 lanes are as fast or
+// faster (1920 columns: 14.1 us for 4446 rows, 14.2 with 128 lanes; one row of
+// 3072: 4.1 and 4.8), except where their last vector would be half empty and
+// rows are many (17776 x 3072: 70.6 us with 128 lanes, 73.8 with 256; 512 rows
+// 6.1 and 5.3).
+template <bool NTL>
+static hipError_t launch_rows(const RnParams& p, int fmt, hipStream_t st) {
+  const int K = p.K;
+  if (K <= 64) return launch_fmt<8, 1, NTL>(p, fmt, st);
+  if (K <= 128) return launch_fmt<16, 1, NTL>(p, fmt, st);
+  if (K <= 256 && p.b <= 128) return launch_fmt<16, 2, NTL>(p, fmt, st);
+  if (K <= 512) return launch_fmt<64, 1, NTL>(p, fmt, st);
+  if (K <= 1024) return launch_fmt<64, 2, NTL>(p, fmt, st);
+  if (K <= 2048) return launch_fmt<256, 1, NTL>(p, fmt, st);
+  if (K <= 3072 && p.M >= 1024) return launch_fmt<128, 3, NTL>(p, fmt, st);
+  if (K <= 4096) return launch_fmt<256, 2, NTL>(p, fmt, st);
+  if (K <= 6144) return launch_fmt<256, 3, NTL>(p, fmt, st);
+  if (K <= 8192) return launch_fmt<256, 4, NTL>(p, fmt, st);
+  if (K <= 12288) return launch_fmt<256, 6, NTL>(p, fmt, st);
+  return launch_fmt<256, 8, NTL>(p, fmt, st);
 }
 
 hipError_t launch_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, const void* res, int64_t ldr,
@@ -316,18 +369,11 @@ hipError_t launch_rmsnorm_quantize(const void* x, int64_t M, int64_t K, int64_t 
   p.had_shift = b == 16 ? 2 : b == 64 ? 3 : b == 256 ? 4 : 0;
   p.had_scale = b == 32 ? HadScale<32>::f : b == 128 ? HadScale<128>::f : 1.0f;
   p.M = (int32_t)M; p.K = (int32_t)K; p.b = b;
-  const char* tv = getenv("ROWS");
-  const int v = tv ? atoi(tv) : 0;
-  if (v == 1) {
-    if (K <= 1024) return launch_fmt<64, 2>(p, fmt, st);
-    if (K <= 2048) return launch_fmt<64, 4>(p, fmt, st);
-    if (K <= 3072) return launch_fmt<64, 6>(p, fmt, st);
-    if (K <= 4096) return launch_fmt<64, 8>(p, fmt, st);
-  }
-  if (K <= 2048) return launch_fmt<256, 1>(p, fmt, st);
-  if (K <= 4096) return launch_fmt<256, 2>(p, fmt, st);
-  if (K <= 8192) return launch_fmt<256, 4>(p, fmt, st);
-  return launch_fmt<256, 8>(p, fmt, st);
+  // Inputs that cannot stay in the 256 MB cache in front of memory are read
+  // past it (72.9 -> 70.6 us for 384 MB in all, 17776 x 3072); smaller ones
+  // may come from it (4446 x 1920, 60 MB: 14.1 us cached, 15.0 past it).
+  const int64_t bytes = M * K * (2 + (res ? 2 : 0) + (sum ? 2 : 0) + (fmt == VDTQ_FMT_BF16 ? 2 : 1));
+  return bytes > (int64_t(256) << 20) ? launch_rows<true>(p, fmt, st) : launch_rows<false>(p, fmt, st);
 }
 
 }  // namespace vdtq
