@@ -31,11 +31,11 @@ def _stream(dev: torch.device):
 def _launch(fn, dev: torch.device, *args):
     """Calls an entry point with dev current (a launch needs its stream's
     device to be the current one) and the stream as its last argument."""
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(dev))
-    else:
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(dev))
+    else:
+        rc = fn(*args, _stream(dev))
     if rc != L.OK:
         L.check(rc)
 
@@ -56,8 +56,8 @@ def _buf(t, name: str, dtype, shape, dev: torch.device):
     """A caller-given buffer the library reads or writes as a dense row-major
     array: it must be a contiguous tensor of exactly `shape` and `dtype` on
     `dev`, or the kernel would read or write past it."""
-    if (type(t) is torch.Tensor and t.dtype == dtype and t.shape == shape and t.device == dev
-            and dev.type == _DEVICE_TYPE and t.is_contiguous()):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev
+            and dev.type == _DEVICE_TYPE):
         return t
     _require(t, dtype, name)
     if t.device != dev:
@@ -402,24 +402,19 @@ def qgemm_mx_quant(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None
     return out
 
 
-def _rows(t: torch.Tensor, name: str, M: int, K: int, dev: torch.device):
-    """A bf16 [M, K] tensor on dev with unit column stride (its row stride is
-    passed on)."""
-    if (type(t) is torch.Tensor and t.dtype == torch.bfloat16 and t.shape == (M, K) and t.device == dev
-            and dev.type == _DEVICE_TYPE and t.is_contiguous()):
-        return t
+def _rows(t: torch.Tensor, name: str, M: int, K: int, dev: torch.device) -> int:
+    """Checks a bf16 [M, K] tensor on dev with unit column stride; returns its
+    row stride (a single row's means nothing: K)."""
+    if (type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.shape == (M, K) and t.is_contiguous()
+            and t.device == dev and dev.type == _DEVICE_TYPE):
+        return K
     _require(t, torch.bfloat16, name)
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if tuple(t.shape) != (M, K) or (K > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [{M}, {K}] with unit column stride, got shape {tuple(t.shape)} "
                          f"strides {tuple(t.stride())}")
-    return t
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride in elements; the stride of a single row means nothing."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if M > 1 else K
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -435,7 +430,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         raise ValueError("x must be a 2-D device tensor")
     M, K = x.shape
     dev = x.device
-    _rows(x, "x", M, K, dev)
+    ldx = _rows(x, "x", M, K, dev)
     if fmt not in ("int8", "bf16", "mxfp4", "mxfp8"):
         raise ValueError(f"fmt {fmt!r}")
     if K % 16 or (fmt in ("mxfp4", "mxfp8") and K % 32):
@@ -444,10 +439,11 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         _buf(weight, "weight", torch.float32, (K,), dev)
     ldr = lds = 0
     if residual is not None:
-        ldr = _row_stride(_rows(residual, "residual", M, K, dev))
+        ldr = _rows(residual, "residual", M, K, dev)
         if sum_out is None:
-            sum_out = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-        lds = _row_stride(_rows(sum_out, "sum_out", M, K, dev))
+            sum_out, lds = torch.empty(M, K, dtype=torch.bfloat16, device=dev), K
+        else:
+            lds = _rows(sum_out, "sum_out", M, K, dev)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if fmt == "int8":
@@ -473,8 +469,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         else:
             _mx(out, "out", M, K, dev)
         fcode, s = L.FMT_MXFP4 if fmt == "mxfp4" else L.FMT_MXFP8, out.scales
-    _launch(L.lib().rmsnorm_quantize, dev, _p(x), M, K, _row_stride(x), _p(residual), ldr, _p(weight), eps, had_block,
-            fcode, _p(sum_out), lds, _p(out.q), _p(s))
+    _launch(L.lib().rmsnorm_quantize, dev, x.data_ptr(), M, K, ldx, _p(residual), ldr, _p(weight), eps, had_block,
+            fcode, _p(sum_out), lds, out.q.data_ptr(), _p(s))
     return out, sum_out
 
 
@@ -488,8 +484,8 @@ def qgemv_w4a16(a: BF16Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = No
     _nvfp4(w, "w", N, K, dev)
     _bias(bias, N, dev)
     y, ldy, od = _result(M, N, out_dtype, dev, y)
-    _launch(L.lib().qgemv_w4a16, dev, _p(a.q), _p(w.q), _p(w.scales), _p(w.ts), _p(bias), _p(y), ldy, od, M,
-            N, K)
+    _launch(L.lib().qgemv_w4a16, dev, a.q.data_ptr(), w.q.data_ptr(), w.scales.data_ptr(), w.ts.data_ptr(),
+            _p(bias), y.data_ptr(), ldy, od, M, N, K)
     return y
 
 
@@ -504,8 +500,8 @@ def qgemv_w4a8(a: INT8Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = Non
     _nvfp4(w, "w", N, K, dev)
     _bias(bias, N, dev)
     y, ldy, od = _result(M, N, out_dtype, dev, y)
-    _launch(L.lib().qgemv_w4a8, dev, _p(a.q), _p(a.scales), _p(w.q), _p(w.scales), _p(w.ts), _p(bias), _p(y),
-            ldy, od, M, N, K)
+    _launch(L.lib().qgemv_w4a8, dev, a.q.data_ptr(), a.scales.data_ptr(), w.q.data_ptr(), w.scales.data_ptr(),
+            w.ts.data_ptr(), _p(bias), y.data_ptr(), ldy, od, M, N, K)
     return y
 
 
@@ -523,8 +519,8 @@ def qgemv_mx(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None,
     _mx(w, "w", N, K, dev)
     _bias(bias, N, dev)
     y, ldy, od = _result(M, N, out_dtype, dev, y)
-    _launch(L.lib().qgemv_mx, dev, L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, _p(a.q), _p(a.scales),
-            _p(w.q), _p(w.scales), _p(bias), _p(y), ldy, od, M, N, K)
+    _launch(L.lib().qgemv_mx, dev, L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, a.q.data_ptr(),
+            a.scales.data_ptr(), w.q.data_ptr(), w.scales.data_ptr(), _p(bias), y.data_ptr(), ldy, od, M, N, K)
     return y
 
 
@@ -554,8 +550,9 @@ def qgemm_mx_grouped(a: MXTensor, w: MXTensor, offsets: torch.Tensor, bias: Opti
     if bias is not None:
         _buf(bias, "bias", torch.float32, (E, N), dev)
     y, ldy, od = _result(T, N, out_dtype, dev, y)
-    _launch(L.lib().qgemm_mx_grouped, dev, L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, _p(a.q),
-            _p(a.scales), _p(w.q), _p(w.scales), _p(bias), _p(offsets), E, _p(y), ldy, od, T, N, K)
+    _launch(L.lib().qgemm_mx_grouped, dev, L.FMT_MXFP4 if a.fmt == "mxfp4" else L.FMT_MXFP8, a.q.data_ptr(),
+            a.scales.data_ptr(), w.q.data_ptr(), w.scales.data_ptr(), _p(bias), offsets.data_ptr(), E, y.data_ptr(),
+            ldy, od, T, N, K)
     return y
 
 
