@@ -426,8 +426,8 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * No workspace.  A NaN in an activation row, in its scale (INT8) or an
  * 0xFF scale byte (MX) makes that row of Y NaN and no other.
  * Errors: VDTQ_EINVAL for null or misaligned pointers, bad sizes or
- * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS or
- * K > 2^25.
+ * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS,
+ * K > 2^24 or N >= 2^26.
  */
 #define VDTQ_GEMV_MAX_ROWS 32
 int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev,
@@ -454,6 +454,12 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  *
  * Defined by: [gist] §2.A / §3.1 and §4 as for qgemm_mx.
  *
+ * Products and sums: fp32 output, and bf16 output of MXFP4 activations: exact
+ * products, added in fp32.  bf16 output of MXFP8 activations: as qgemm_mx, the
+ * block-scaled matrix instruction, which cuts each of 8 consecutive products
+ * at 2^-13 of the power of two below the largest of them (3.4e-5 of the
+ * result's norm on typical rows; half a bf16 step is 2e-3).
+ *
  * a_fmt          VDTQ_FMT_MXFP4 or VDTQ_FMT_MXFP8
  * a_q_dev, a_s_dev  [T] rows as for qgemm_mx
  * w_q_dev        uint8 [E][N][K/2] E2M1 codes, w_s_dev uint8 E8M0
@@ -469,7 +475,9 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  * K              > 0, multiple of 32
  * No workspace.
  * Errors: VDTQ_EINVAL for a bad a_fmt or size, null or misaligned pointers,
- * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128 or K > 2^25.
+ * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128, K > 2^24,
+ * N >= 2^26, T > 2^30 or more output tiles than a launch holds (2^24 of 256
+ * rows of an expert x 256 features; with MXFP8 and fp32 output 64 x 128).
  */
 int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
                      const uint8_t* w_q_dev, const uint8_t* w_s_dev,

@@ -67,7 +67,7 @@ def _gemv(fn, **kw):
     (dict(od=2), L.EINVAL), (dict(aq=None), L.EINVAL), (dict(wq=None), L.EINVAL), (dict(ws=None), L.EINVAL),
     (dict(y=None), L.EINVAL), (dict(aq=ODD), L.EINVAL), (dict(wq=ODD), L.EINVAL), (dict(M=33), L.EUNSUPPORTED),
     (dict(bias=ctypes.c_void_p(0x100002)), L.EINVAL), (dict(M=1 << 31), L.EINVAL),
-    (dict(K=(1 << 25) + 128), L.EUNSUPPORTED),
+    (dict(K=(1 << 24) + 128), L.EUNSUPPORTED), (dict(N=1 << 26, ldy=1 << 26), L.EUNSUPPORTED),
 ])
 def test_qgemv_rejects(fn, kw, code):
     assert _gemv(fn, **kw) == code
@@ -93,10 +93,12 @@ def _grp(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(fmt=L.FMT_NVFP4), L.EINVAL), (dict(E=-1), L.EINVAL), (dict(E=65537), L.EINVAL), (dict(K=0), L.EINVAL),
-    (dict(K=48), L.EINVAL), (dict(K=96), L.EUNSUPPORTED), (dict(K=(1 << 25) + 128), L.EUNSUPPORTED), (dict(T=-1), L.EINVAL), (dict(N=-1), L.EINVAL),
+    (dict(K=48), L.EINVAL), (dict(K=96), L.EUNSUPPORTED), (dict(K=(1 << 24) + 128), L.EUNSUPPORTED), (dict(T=-1), L.EINVAL), (dict(N=-1), L.EINVAL),
     (dict(ldy=10), L.EINVAL), (dict(od=3), L.EINVAL), (dict(off=None), L.EINVAL), (dict(aq=None), L.EINVAL),
     (dict(as_=None), L.EINVAL), (dict(wq=None), L.EINVAL), (dict(ws=None), L.EINVAL), (dict(y=None), L.EINVAL),
-    (dict(aq=ODD), L.EINVAL), (dict(off=ctypes.c_void_p(0x100002)), L.EINVAL),
+    (dict(aq=ODD), L.EINVAL), (dict(off=ctypes.c_void_p(0x100002)), L.EINVAL), (dict(T=(1 << 30) + 1), L.EUNSUPPORTED),
+    (dict(N=1 << 26, ldy=1 << 26), L.EUNSUPPORTED), (dict(T=1 << 30, N=4096, ldy=4096), L.EUNSUPPORTED),
+    (dict(T=1 << 24, N=8192, ldy=8192, od=1), L.EUNSUPPORTED),
 ])
 def test_grouped_rejects(kw, code):
     assert _grp(**kw) == code

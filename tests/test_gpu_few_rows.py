@@ -229,6 +229,52 @@ def test_grouped_sizes(afmt, N, K, counts):
     check_grouped(afmt, counts, N, K, front=3, back=5)
 
 
+@pytest.mark.parametrize("afmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("K", [7168, 7296, 12288, 14336, 14464])
+def test_grouped_long_rows(afmt, K):
+    """K around the borders where the few-row kernel takes K in two turns
+    and where it gives way to tiles."""
+    need_gpu()
+    check_grouped(afmt, [3, 0, 12, 1], 40, K)
+
+
+@pytest.mark.parametrize("afmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("counts", [[12], [13], [12, 12], [13, 13], [191], [192], [191, 191], [192, 192], [0, 0, 0, 40],
+                                    [200, 1, 1, 1], [1, 1, 500]])
+def test_grouped_borders_of_the_kernels(afmt, counts):
+    need_gpu()
+    check_grouped(afmt, counts, 136, 640, back=2)
+
+
+@pytest.mark.parametrize("kind", ["mxfp8", "mxfp4"])
+def test_scales_far_from_one(kind):
+    """Block scales of 2^-60 and 2^50 against weights of 2^40 and 2^-30."""
+    need_gpu()
+    rng = rng_of(26)
+    for T, E in ((5, 1), (40, 2), (500, 2)):
+        N, K = 48, 512
+        (aq, as_), ad = acts(rng, T, K, kind)
+        (wq, ws), wd = weights(rng, E * N, K, "mx")
+        as_ = as_.copy()
+        ws = ws.copy()
+        as_[:, 0::2] -= 60
+        ws[:, 0::2] += 40
+        as_[:, 1::2] += 50
+        ws[:, 1::2] -= 30
+        ad.scales.copy_(dev(as_))
+        wd.scales.copy_(dev(ws))
+        off = np.array([0, T] if E == 1 else [0, T // 3, T], np.int32)
+        want, _ = G.qgemm_mx_grouped(aq, as_, kind, wq, ws, off)
+        y = V.qgemm_mx_grouped(ad, wd, dev(off), None, "f32")
+        torch.cuda.synchronize()
+        for e in range(E):
+            r, w = slice(off[e], off[e + 1]), slice(e * N, (e + 1) * N)
+            t = terms_mx(aq[r], as_[r], kind, wq[w], ws[w], None)
+            assert_elementwise(values(y)[r], want[r], t, K, "f32", kind)
+        if T <= 32 and E == 1:
+            assert_elementwise(values(V.qgemv_mx(ad, wd, None, "f32")), want, t, K, "f32", kind)
+
+
 def test_grouped_many_experts():
     need_gpu()
     c = rng_of(21).integers(0, 4, size=300).tolist()
@@ -277,7 +323,7 @@ def test_grouped_output_strides():
 def test_grouped_rows_that_are_not_finite():
     need_gpu()
     rng = rng_of(24)
-    for counts in ([3, 4, 2], [150, 140]):
+    for counts in ([3, 4, 2], [150, 140], [400, 390]):
         T, N, K = sum(counts), 80, 256
         _, ad = acts(rng, T, K, "mxfp8")
         _, wd = weights(rng, len(counts) * N, K, "mx")
@@ -357,6 +403,68 @@ def test_chain_against_the_oracle():
     cut = np.concatenate([cut_off(om["q"][a:b], om["scales"][a:b], whe[0][e * N:(e + 1) * N], whe[1][e * N:(e + 1) * N])
                           for e, (a, b) in enumerate(zip(off[:-1], off[1:])) if b > a])
     assert_elementwise(values(got[4]), want, te + cut / (2 * (K + 4) * 2.0 ** -24), K, "bf16")
+
+
+_FIRST_CALLS_UNDER_CAPTURE = r"""
+import sys
+import torch
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_gpu_few_rows as T
+ins = T.chain_inputs(51, M=30)[1]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = T.chain(*ins)                      # the process's first calls
+for _ in range(3):
+    g.replay()
+    torch.cuda.synchronize()
+    want = T.chain(*ins)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+print("ok")
+"""
+
+
+def test_first_calls_under_capture():
+    """Nothing that a first call sets up is missing from a graph that was
+    captured before any eager call (in a fresh process)."""
+    need_gpu()
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS_UNDER_CAPTURE, root], capture_output=True, text=True, timeout=110)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-2000:] + r.stderr[-2000:]
+
+
+def test_chain_from_two_threads():
+    """Two host threads, a stream each, the same operands read by both: the
+    bits of a lone call."""
+    need_gpu()
+    import threading
+    ins = chain_inputs(61)[1]
+    want = [t.clone() for t in chain(*ins)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(10):
+                    got = chain(*ins)
+                    s.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        bad.append(k)
+        except Exception as e:                   # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
 
 
 def test_chain_in_graphs_and_on_two_streams():

@@ -147,6 +147,35 @@ def test_stream_updated_in_place(which, M, K):
     assert np.array_equal(host_bits(dst), o["r"])
 
 
+@pytest.mark.parametrize("M,K,b", [(9, 256, 128), (300, 512, 256), (1024, 2064, 16), (1023, 3056, 16), (1500, 2560, 64),
+                                   (5, 5120, 256), (6, 6144, 64), (6, 6160, 16), (3, 8192, 128), (3, 10240, 64),
+                                   (70, 1040, 16), (3000, 64, 32), (900, 48, 16)])
+def test_borders_of_the_lane_counts(M, K, b):
+    need_gpu()
+    for fmt in ("int8", "bf16") if K % 32 else FMTS:
+        check(M, K, b, fmt, seed=M)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mxfp8", "bf16"])
+@pytest.mark.parametrize("M,K", [(17776, 3072), (21000, 2048), (12000, 6144), (700000, 64)])
+def test_large_inputs_are_their_parts(M, K, fmt):
+    """Above 256 MB the inputs are read past the cache: the bits are those
+    of the same rows in small calls."""
+    need_gpu()
+    log(f"large {M} x {K} {fmt}")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = (torch.randn(M, K, device="cuda", generator=g) * 3).bfloat16()
+    r = (torch.randn(M, K, device="cuda", generator=g) * 3).bfloat16()
+    w = 1 + 0.1 * torch.randn(K, device="cuda", generator=g)
+    whole, s = V.rmsnorm_quantize(x, w, r, EPS, 64, fmt)
+    for a in range(0, M, M // 5 + 1):
+        b = min(M, a + M // 5 + 1)
+        part, t = V.rmsnorm_quantize(x[a:b], w, r[a:b], EPS, 64, fmt)
+        assert torch.equal(part.q.view(torch.uint8), whole.q[a:b].view(torch.uint8)) and torch.equal(t, s[a:b])
+        if fmt != "bf16":
+            assert torch.equal(part.scales, whole.scales[a:b])
+
+
 def test_no_rows():
     need_gpu()
     x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")

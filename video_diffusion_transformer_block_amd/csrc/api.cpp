@@ -338,7 +338,8 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
   if (!a_q || !a_s || !w_q || !w_s || !y) return fail(VDTQ_EINVAL, "%s: null pointer argument", name);
   if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(y, out_dtype ? 4 : 2) || (bias && !aligned(bias, 4)))
     return fail(VDTQ_EINVAL, "%s: misaligned pointer (codes need 16 bytes)", name);
-  if (K > (1 << 25)) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is above 2^25", name, (long long)K);
+  if (K > (1 << 24)) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is above 2^24", name, (long long)K);
+  if (N >= (1 << 26)) return fail(VDTQ_EUNSUPPORTED, "%s: N=%lld is not below 2^26", name, (long long)N);
   return VDTQ_OK;
 }
 
@@ -401,8 +402,10 @@ int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, 
   if (!offsets_dev || !aligned(offsets_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned offsets", name);
   if (!aligned(a_s_dev, 4) || !aligned(w_s_dev, 4)) return fail(VDTQ_EINVAL, "%s: scales need 4 bytes alignment", name);
   if (K % 128) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is not a multiple of 128", name, (long long)K);
-  // row tiles (of 16 rows at least) and feature tiles (of 16) are counted in 31 bits
-  if ((T / 16 + E) * ((N + 15) / 16) > kI32) return fail(VDTQ_EUNSUPPORTED, "%s: too many output tiles", name);
+  if (T > (1 << 30)) return fail(VDTQ_EUNSUPPORTED, "%s: T=%lld is above 2^30", name, (long long)T);
+  const bool exact = a_fmt == VDTQ_FMT_MXFP8 && out_dtype == VDTQ_OUT_F32;
+  if (!vdtq::grouped_tiles_fit(T, E, N, exact ? 64 : 256, exact ? 128 : 256))
+    return fail(VDTQ_EUNSUPPORTED, "%s: too many output tiles", name);
   const vdtq::MxGrouped q{a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, offsets_dev, y_dev, ldy,
                           (int32_t)T, (int32_t)N, (int32_t)K, (int32_t)E, out_dtype == VDTQ_OUT_F32};
   hipError_t e = vdtq::launch_qgemm_mx_grouped(a_fmt == VDTQ_FMT_MXFP8, q, static_cast<hipStream_t>(stream));

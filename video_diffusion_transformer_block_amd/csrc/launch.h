@@ -101,6 +101,11 @@ struct MxGrouped {
   int32_t T, N, K, E;
   int32_t out_f32;
 };
+// Whether a launch can hold the tiles of bm rows x bn features (of 256
+// threads; a launch counts its threads in 32 bits).
+inline bool grouped_tiles_fit(int64_t T, int64_t E, int64_t N, int bm, int bn) {
+  return (T / bm + E) * ((N + bn - 1) / bn) < (int64_t(1) << 24);
+}
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st);
 hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const MxGrouped& q, hipStream_t st);
 hipError_t launch_qgemm_mx_grouped_exact(const MxGrouped& q, hipStream_t st);

@@ -498,17 +498,19 @@ hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t s
   //   7680 x 1920 x 8     17, 19            20, 19            23, 19   36, 38           69, 69
   //   3072 x 12288 x 8    41, 57            55, 57            80, 60   88, 150          -
   const int avg = q.T / q.E;
+  // the few-row kernels count row tiles in the launch's y, which ends at 2^16
+  const bool few = avg <= 12 && q.T / 16 + q.E < 65536;
   // fp32 output of MXFP8 rows: sums of exact products, which the block-scaled
   // instruction does not form.  8 rows an expert: 17 us by the few-row kernel,
   // 27 by tiles (1920 x 3072 x 16), 58 and 78 (3072 x 12288 x 8); 16 rows: 28
   // and 27, 87 and 80; tiles of 128 x 128 are 8 % faster at thousands of rows,
   // 40 % slower below 64
   if (a_fp8 && q.out_f32) {
-    if (avg <= 12) return launch_qgemm_mx_grouped_exact(q, st);
+    if (few) return launch_qgemm_mx_grouped_exact(q, st);
     return launch_tile<true, 64, 128, 2, true>(q, st);
   }
-  if (avg >= 192) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
-  if (avg <= 12 && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
+  if (avg >= 192 || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
+  if (few && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
   // three stages where three workgroups still fit a compute unit
   return a_fp8 ? launch_tile<true, 64, 128, 2>(q, st) : launch_tile<false, 64, 128, 3>(q, st);
 }

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(rn_threads(T)) void rmsnorm_quantize_kernel(RnParam
   __shared__ double sum_slot[4];
   __shared__ float max_slot[4];
   const int t = threadIdx.x % T;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / T;
   const bool live = row < p.M;                      // the lanes of a row past M hold zeros
   const int nv = p.K / 8;
 
@@ -318,7 +318,9 @@ __global__ __launch_bounds__(rn_threads(T)) void rmsnorm_quantize_kernel(RnParam
 template <int T, int C, bool NTL>
 static hipError_t launch_fmt(const RnParams& p, int fmt, hipStream_t st) {
   constexpr int B = rn_threads(T), ROWS = B / T;
-  const dim3 grid((unsigned)(((int64_t)p.M + ROWS - 1) / ROWS)), block(B);
+  // a launch counts the threads of a dimension in 32 bits: rows fold over y
+  const int64_t wgs = ((int64_t)p.M + ROWS - 1) / ROWS, x = wgs < (1 << 22) ? wgs : (1 << 22);
+  const dim3 grid((unsigned)x, (unsigned)((wgs + x - 1) / x)), block(B);
   switch (fmt) {
     case VDTQ_FMT_INT8: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_INT8, NTL>), grid, block, 0, st, p); break;
     case VDTQ_FMT_BF16: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_BF16, NTL>), grid, block, 0, st, p); break;
