@@ -437,6 +437,54 @@ def test_first_calls_under_capture():
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-2000:] + r.stderr[-2000:]
 
 
+def test_native_and_python_marshalling_agree(monkeypatch):
+    """The native entry takes the ordinary calls (given outputs among them)
+    and the Python path gives the same bits; what the native entry declines
+    (strided outputs, refused sizes, wrong types) the Python path does or
+    refuses."""
+    need_gpu()
+    from video_diffusion_transformer_block_amd import ops as O
+    assert O._fast is not None, "the native entry is not built"
+    ins = chain_inputs(62)[1]
+    fast = [t.clone() for t in chain(*ins)]
+    x, res, gain, w8, _, wm, we, off = ins
+    a8, _ = V.rmsnorm_quantize(x, gain, res)
+    y = torch.full((x.shape[0], w8.q.shape[0]), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert V.qgemv_w4a8(a8, w8, y=y) is y and torch.equal(y, fast[1])
+    calls = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*args):
+                r = getattr(O_fast, name)(*args)
+                calls.append((name, r is not None))
+                return r
+            return call
+
+    O_fast = O._fast
+    monkeypatch.setattr(O, "_fast", Spy())
+    again = chain(*ins)
+    assert all(torch.equal(a, b) for a, b in zip(again, fast))
+    assert calls == [("norm", True)] * 3 + [("gemv", True)] * 3 + [("grouped", True)]
+    calls.clear()
+    wide = torch.empty((x.shape[0], y.shape[1] + 4), dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(V.qgemv_w4a8(a8, w8, y=wide[:, :y.shape[1]]), fast[1]) and calls == [("gemv", False)]
+    for bad in (lambda: V.qgemv_w4a8(a8, w8, torch.zeros(3, device="cuda")), lambda: V.qgemv_w4a8(a8, w8, None, "f16"),
+                lambda: V.rmsnorm_quantize(x[:, :24]), lambda: V.rmsnorm_quantize(x, gain[:5]),
+                lambda: V.rmsnorm_quantize(x, gain, None, sum_out=x), lambda: V.rmsnorm_quantize(x.float()),
+                lambda: V.qgemm_mx_grouped(V.rmsnorm_quantize(x, fmt="mxfp8")[0], we, off.long())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: V.rmsnorm_quantize(x, eps=0.0), lambda: V.rmsnorm_quantize(x, had_block=48),
+                lambda: V.qgemv_w4a8(V.INT8Tensor(a8.q.repeat(2, 1), a8.scales.repeat(2)), w8)):
+        with pytest.raises(V.VdtqError):
+            bad()
+    monkeypatch.setattr(O, "_fast", None)
+    slow = chain(*ins)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(slow, fast))
+
+
 def test_chain_from_two_threads():
     """Two host threads, a stream each, the same operands read by both: the
     bits of a lone call."""

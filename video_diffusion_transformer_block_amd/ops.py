@@ -12,6 +12,14 @@ import torch
 
 from . import _lib as L
 
+# The ordinary case of the short calls goes through native marshalling
+# (csrc/fast_calls.cpp); it answers None where it does not apply, and the code
+# here then does the call or says what is wrong with it.
+try:
+    from . import _fastcalls as _fast
+except ImportError:
+    _fast = None
+
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
@@ -417,6 +425,9 @@ def _rows(t: torch.Tensor, name: str, M: int, K: int, dev: torch.device) -> int:
     return t.stride(0) if M > 1 else K
 
 
+_NORM_FMT = {"int8": L.FMT_INT8, "bf16": L.FMT_BF16, "mxfp4": L.FMT_MXFP4, "mxfp8": L.FMT_MXFP8}
+
+
 def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                      residual: Optional[torch.Tensor] = None, eps: float = 1e-6, had_block: int = 64,
                      fmt: str = "int8", out=None, sum_out: Optional[torch.Tensor] = None):
@@ -426,6 +437,12 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     bf16(x + residual), written to sum_out when given (x or residual itself
     updates it in place), or None without a residual.  out: a previously
     returned tensor of the same format and shape whose buffers are reused."""
+    if _fast is not None and out is None and fmt in _NORM_FMT:
+        r = _fast.norm(x, weight, residual, eps, had_block, _NORM_FMT[fmt], sum_out)
+        if r is not None:
+            q, s, total = r
+            t = INT8Tensor(q, s) if fmt == "int8" else BF16Tensor(q) if fmt == "bf16" else MXTensor(q, s, fmt)
+            return t, total
     if not torch.is_tensor(x) or x.dim() != 2:
         raise ValueError("x must be a 2-D device tensor")
     M, K = x.shape
@@ -477,6 +494,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 def qgemv_w4a16(a: BF16Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
                 out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """qgemm_w4a16 for at most 32 rows."""
+    if _fast is not None:
+        r = _fast.gemv(0, a.q, None, w.q, w.scales, w.ts, bias, y, out_dtype)
+        if r is not None:
+            return r
     M, K = a.q.shape
     N = w.q.shape[0]
     dev = a.q.device
@@ -492,6 +513,10 @@ def qgemv_w4a16(a: BF16Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = No
 def qgemv_w4a8(a: INT8Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
                out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """qgemm_w4a8 for at most 32 rows."""
+    if _fast is not None:
+        r = _fast.gemv(1, a.q, a.scales, w.q, w.scales, w.ts, bias, y, out_dtype)
+        if r is not None:
+            return r
     M, K = a.q.shape
     N = w.q.shape[0]
     dev = a.q.device
@@ -505,12 +530,19 @@ def qgemv_w4a8(a: INT8Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = Non
     return y
 
 
+_MX_KIND = {"mxfp8": 2, "mxfp4": 3}
+
+
 def qgemv_mx(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None,
              out_dtype: str = "bf16", y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """qgemm_mx for at most 32 rows, with every product exact and added in
     fp32."""
     if w.fmt != "mxfp4":
         raise ValueError("MX weights must be mxfp4")
+    if _fast is not None and a.fmt in _MX_KIND:
+        r = _fast.gemv(_MX_KIND[a.fmt], a.q, a.scales, w.q, w.scales, None, bias, y, out_dtype)
+        if r is not None:
+            return r
     M = a.q.shape[0]
     K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
     N = w.q.shape[0]
@@ -534,6 +566,10 @@ def qgemm_mx_grouped(a: MXTensor, w: MXTensor, offsets: torch.Tensor, bias: Opti
     (uninitialised in a new y)."""
     if w.fmt != "mxfp4":
         raise ValueError("MX weights must be mxfp4")
+    if _fast is not None and a.fmt in _MX_KIND:
+        r = _fast.grouped(a.fmt == "mxfp8", a.q, a.scales, w.q, w.scales, offsets, bias, y, out_dtype)
+        if r is not None:
+            return r
     T = a.q.shape[0]
     K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
     dev = a.q.device
