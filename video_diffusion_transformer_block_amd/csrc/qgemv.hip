@@ -413,8 +413,13 @@ static hipError_t launch_tiles(GemvParams p, int gy, int tiles, int64_t max_lds,
 
 template <int AF>
 static hipError_t launch_gemv(const GemvParams& p, hipStream_t st) {
-  // one workgroup a compute unit when there are no more: all of its LDS
-  const int64_t lds = (p.N + 15) / 16 > device_cu_count() ? kGvMaxLds / 2 : kGvMaxLds;
+  // LDS for all workgroups to run at once.  12288 features (3 workgroups a
+  // compute unit), K = 3072: 8.8 us with 3 wavefronts of 2 turns against 10.2
+  // with 6 of one (one INT8 row), 12.0 against 14.3 with 160 KB for two (32
+  // MXFP8 rows); 3072 features, K = 12288 (one): 9.9 us with all of it, 10.5
+  // with half (16 MXFP8 rows)
+  const int64_t per_cu = ((p.N + 15) / 16 + device_cu_count() - 1) / device_cu_count();
+  const int64_t lds = kGvMaxLds / std::min<int64_t>(per_cu, 4);
   if (p.M <= 4) return launch_tiles<AF, 4>(p, 1, 1, lds, st);
   return p.M <= 16 ? launch_tiles<AF, 16>(p, 1, 1, lds, st) : launch_tiles<AF, 32>(p, 1, 1, lds, st);
 }
