@@ -205,10 +205,7 @@ void qgemm_mx_kernel(GemmParams p) {
     kb = sl * p.slice_nk;
     ke = min(p.nk, kb + p.slice_nk);
   } else if constexpr (GROUPED) {
-    p.tiles_m = row_tiles(p.offsets, p.experts, p.M, 256);
-    const int tiles = p.tiles_m * p.tiles_n;
-    if ((int)blockIdx.x >= tiles) return;            // the grid is an upper bound
-    tile = xcd_range_id(blockIdx.x, tiles);
+    tile = 0;
     kb = 0;
     ke = p.nk;
   } else {
@@ -217,9 +214,14 @@ void qgemm_mx_kernel(GemmParams p) {
     ke = p.nk;
   }
   int tm, tn;
-  tile_coords(tile, p.tiles_m, p.tiles_n, tm, tn);
   if constexpr (GROUPED) {
-    const RowTile g = row_tile(p.offsets, p.experts, p.M, 256, tm);
+    const RowTile g = pick_row_tile(p.offsets, p.experts, p.M, 256, [&](int tiles_m) {
+      const int tiles = tiles_m * p.tiles_n;
+      if ((int)blockIdx.x >= tiles) return -1;       // the grid is an upper bound
+      tile_coords(xcd_range_id(blockIdx.x, tiles), tiles_m, p.tiles_n, tm, tn);
+      return tm;
+    });
+    if (g.rows <= 0) return;
     p.M = g.rows;
     p.a_q = static_cast<const uint8_t*>(p.a_q) + (int64_t)g.row0 * (A8 ? K : K / 2);
     p.a_s = static_cast<const uint8_t*>(p.a_s) + (int64_t)g.row0 * (K / 32);
@@ -228,6 +230,8 @@ void qgemm_mx_kernel(GemmParams p) {
     if (p.bias) p.bias += (int64_t)g.expert * p.N;
     p.y = static_cast<uint8_t*>(p.y) + (int64_t)g.row0 * p.ldy * (p.out_f32 ? 4 : 2);
     tm = 0;
+  } else {
+    tile_coords(tile, p.tiles_m, p.tiles_n, tm, tn);
   }
   const int m0 = tm * 256, n0 = tn * 256;
 

@@ -244,12 +244,16 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   const int wm = wv >> 1, wn = wv & 1, r32 = lane & 31, h = lane >> 5;
   const int K = p.K, N = p.N, nk = K / 128;
   const int tiles_n = (N + BN - 1) / BN;
-  const int total = row_tiles(p.offsets, p.E, p.T, BM) * tiles_n;
-  if ((int)blockIdx.x >= total) return;         // the grid is an upper bound
-  const int id = xcd_range_id(blockIdx.x, total);
-  // (quotients come from the vector unit: the bases of the loads need scalars)
-  const int along = __builtin_amdgcn_readfirstlane(id / tiles_n);
-  const RowTile t = row_tile(p.offsets, p.E, p.T, BM, along);
+  int id = 0, along = 0;
+  const RowTile t = pick_row_tile(p.offsets, p.E, p.T, BM, [&](int tiles_m) {
+    const int total = tiles_m * tiles_n;
+    if ((int)blockIdx.x >= total) return -1;    // the grid is an upper bound
+    id = xcd_range_id(blockIdx.x, total);
+    // (quotients come from the vector unit: the bases of the loads need scalars)
+    along = __builtin_amdgcn_readfirstlane(id / tiles_n);
+    return along;
+  });
+  if (t.rows <= 0) return;
   // the expert's tiles: groups of 8 row tiles walked along the features
   const int first = t.row0 - (along - t.before) * BM, all = t.row0 + t.rows;
   int tm, tn;

@@ -65,7 +65,22 @@ __device__ __forceinline__ int row_tiles(const int32_t* offsets, int E, int T, i
   return __builtin_amdgcn_readfirstlane(n);
 }
 
-// Tile t (0 <= t < row_tiles).
+// The tile among 64 experts from e0 (lane i: expert e0 + i, rows lo .. hi - 1,
+// `upto` tiles with it) after `past` tiles of earlier ones.
+__device__ __forceinline__ RowTile tile_among(int e0, int lo, int hi, int upto, int past, int bm, int t) {
+  const int i = __builtin_ctzll(__ballot(past + upto > t));   // the first lane whose tiles reach past t
+  const int before = past + (i ? __shfl(upto, i - 1, 64) : 0);
+  const int row0 = __shfl(lo, i, 64) + (t - before) * bm;
+  return RowTile{e0 + i, row0, __shfl(hi, i, 64) - row0, before, past + __shfl(upto, i, 64) - before};
+}
+
+__device__ __forceinline__ RowTile uniform(const RowTile& r) {
+  return RowTile{(int)__builtin_amdgcn_readfirstlane(r.expert), (int)__builtin_amdgcn_readfirstlane(r.row0),
+                 (int)__builtin_amdgcn_readfirstlane(r.rows), (int)__builtin_amdgcn_readfirstlane(r.before),
+                 (int)__builtin_amdgcn_readfirstlane(r.tiles)};
+}
+
+// Tile t; no rows when there are not so many.
 __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int E, int T, int bm, int t) {
   RowTile r{0, 0, 0, 0, 0};
   int past = 0;                                         // tiles of the 64s before
@@ -75,18 +90,27 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int E, int T
       past += all;
       return false;
     }
-    const int i = __builtin_ctzll(__ballot(past + upto > t));   // the first lane whose tiles reach past t
-    const int before = past + (i ? __shfl(upto, i - 1, 64) : 0);
-    const int row0 = __shfl(lo, i, 64) + (t - before) * bm;
-    r = RowTile{e0 + i, row0, __shfl(hi, i, 64) - row0, before, past + __shfl(upto, i, 64) - before};
+    r = tile_among(e0, lo, hi, upto, past, bm, t);
     return true;
   });
-  r.expert = __builtin_amdgcn_readfirstlane(r.expert);
-  r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
-  r.rows = __builtin_amdgcn_readfirstlane(r.rows);
-  r.before = __builtin_amdgcn_readfirstlane(r.before);
-  r.tiles = __builtin_amdgcn_readfirstlane(r.tiles);
-  return r;
+  return uniform(r);
+}
+
+// The tile pick(tiles of all experts) asks for; none where it answers -1.
+// The offsets of up to 64 experts are read once.
+template <class F>
+__device__ __forceinline__ RowTile pick_row_tile(const int32_t* offsets, int E, int T, int bm, F pick) {
+  if (E <= 64) {
+    RowTile r{0, 0, 0, 0, 0};
+    each_group(offsets, E, T, bm, [&](int e0, int lo, int hi, int upto) {
+      const int t = pick((int)__builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64)));
+      if (t >= 0) r = tile_among(e0, lo, hi, upto, 0, bm, t);
+      return true;
+    });
+    return uniform(r);
+  }
+  const int t = pick(row_tiles(offsets, E, T, bm));
+  return t >= 0 ? row_tile(offsets, E, T, bm, t) : RowTile{0, 0, 0, 0, 0};
 }
 
 }  // namespace vdtq
