@@ -385,7 +385,8 @@ int qgemm_mx_quant(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  * K              columns, > 0, <= 16384, a multiple of 16 and of had_block;
  *                for MXFP4 / MXFP8 a multiple of 32
  * residual_dev   bf16 [M][ldr] (ldr as ldx) or NULL
- * weight_dev     float [K] or NULL (ones); finite
+ * weight_dev     float [K] or NULL (ones); finite, and such that y stays
+ *                finite (else that row's codes are unspecified)
  * eps            > 0, finite
  * had_block      16, 32, 64, 128 or 256
  * fmt            VDTQ_FMT_INT8, VDTQ_FMT_BF16, VDTQ_FMT_MXFP4 or
@@ -421,8 +422,9 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * the activations of [gist] §2.A and §2.C.
  *
  * Operands as for the call of the same name, except: M <=
- * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); scales
- * need no alignment; N * K / 2 has no limit below the memory's.
+ * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); with K a
+ * multiple of 128 the scales are 8-byte (NVFP4) or 4-byte (MX) aligned, else
+ * they need no alignment; N * K / 2 has no limit below the memory's.
  * No workspace.  A NaN in an activation row, in its scale (INT8) or an
  * 0xFF scale byte (MX) makes that row of Y NaN and no other.
  * Errors: VDTQ_EINVAL for null or misaligned pointers, bad sizes or

@@ -78,6 +78,10 @@ def test_qgemv_format_rules():
     assert _gemv("mx", fmt=L.FMT_INT8) == L.EINVAL
     assert _gemv("mx", K=48) == L.EINVAL
     assert _gemv("w4a16", wts=None) == L.EINVAL and _gemv("w4a8", wts=None) == L.EINVAL
+    odd = ctypes.c_void_p(0x100002)
+    for fn in ("w4a16", "w4a8", "mx"):                       # scale runs need alignment, bytes do not
+        assert _gemv(fn, K=128, ws=odd) == L.EINVAL
+    assert _gemv("w4a16", K=256, ws=ctypes.c_void_p(0x100004)) == L.EINVAL and _gemv("mx", K=128, as_=odd) == L.EINVAL
     assert _gemv("w4a8", as_=None) == L.EINVAL and _gemv("mx", as_=None) == L.EINVAL
     for fn in ("w4a16", "w4a8", "mx"):
         assert _gemv(fn, M=0, aq=None) == L.OK and _gemv(fn, N=0, y=None) == L.OK

@@ -125,6 +125,25 @@ def test_gemv_output_in_a_wider_tensor(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_gemv_weights_inside_larger_ones(kind):
+    """Rows cut out of stacked weights: scales that start at odd bytes where
+    K is no multiple of 128, and row views where it is."""
+    need_gpu()
+    rng = rng_of(14)
+    for N, K, skip in ((40, 96, 1), (33, 160, 3), (24, 1920, 5), (24, 640, 2)):
+        ah, ad = acts(rng, 5, K, kind)
+        wh, wd = weights(rng, N, K, "mx" if kind.startswith("mx") else "nv")
+        g = K // (32 if kind.startswith("mx") else 16)
+        codes = torch.zeros((N + 16) * K // 2, dtype=torch.uint8, device="cuda")
+        codes[8 * K:8 * K + N * K // 2] = wd.q.flatten()              # 16 rows of K / 2 bytes in
+        scales = torch.zeros((N + 16) * g, dtype=torch.uint8, device="cuda")
+        scales[skip * g:(skip + N) * g] = wd.scales.flatten()
+        q, s = codes[8 * K:8 * K + N * K // 2].view(N, K // 2), scales[skip * g:(skip + N) * g].view(N, g)
+        w = V.MXTensor(q, s, "mxfp4") if kind.startswith("mx") else V.NVFP4Tensor(q, s, wd.ts)
+        assert torch.equal(CALL[kind](ad, w, None, "f32"), CALL[kind](ad, wd, None, "f32"))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_gemv_rows_that_are_not_finite(kind):
     """A NaN (bf16), a NaN scale (INT8) or an 0xFF scale byte (MX) makes its
     row of Y NaN; the other rows keep their bits."""

@@ -343,9 +343,13 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
   return VDTQ_OK;
 }
 
-static int gemv_rows(const char* name, int64_t M) {
+// The further checks of the few-row products.  With K a multiple of 128 the
+// scales are read as 8-byte (NVFP4) or 4-byte (MX) runs, else byte by byte.
+static int gemv_check(const char* name, int64_t M, int64_t K, const void* w_s, const void* a_s, int run) {
   if (M > VDTQ_GEMV_MAX_ROWS)
     return fail(VDTQ_EUNSUPPORTED, "%s: M=%lld is more than %d rows", name, (long long)M, VDTQ_GEMV_MAX_ROWS);
+  if (K % 128 == 0 && (!aligned(w_s, run) || !aligned(a_s, run)))
+    return fail(VDTQ_EINVAL, "%s: scales need %d bytes alignment", name, run);
   return VDTQ_OK;
 }
 
@@ -354,7 +358,7 @@ int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev, const uint8_t* w_s_de
                 void* stream) {
   const char* name = "qgemv_w4a16";
   int rc = small_check(name, a_dev, a_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
-  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (rc || (rc = gemv_check(name, M, K, w_s_dev, nullptr, 8))) return rc;
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned w_ts", name);
   hipError_t e = vdtq::launch_qgemv(0, a_dev, nullptr, w_q_dev, w_s_dev, w_ts_dev, bias_dev, y_dev, ldy, out_dtype, M,
@@ -367,7 +371,7 @@ int qgemv_w4a8(const int8_t* a_q_dev, const float* a_s_dev, const uint8_t* w_q_d
                int64_t N, int64_t K, void* stream) {
   const char* name = "qgemv_w4a8";
   int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
-  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (rc || (rc = gemv_check(name, M, K, w_s_dev, nullptr, 8))) return rc;
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4) || !aligned(a_s_dev, 4))
     return fail(VDTQ_EINVAL, "%s: null w_ts or misaligned w_ts / a_s", name);
@@ -382,7 +386,7 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, const ui
   const char* name = "qgemv_mx";
   if (a_fmt != VDTQ_FMT_MXFP4 && a_fmt != VDTQ_FMT_MXFP8) return fail(VDTQ_EINVAL, "%s: a_fmt=%d", name, a_fmt);
   int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 32);
-  if (rc || (rc = gemv_rows(name, M))) return rc;
+  if (rc || (rc = gemv_check(name, M, K, w_s_dev, a_s_dev, 4))) return rc;
   if (M == 0 || N == 0) return ok();
   hipError_t e = vdtq::launch_qgemv(a_fmt == VDTQ_FMT_MXFP8 ? 2 : 3, a_q_dev, a_s_dev, w_q_dev, w_s_dev, nullptr,
                                     bias_dev, y_dev, ldy, out_dtype, M, N, K, static_cast<hipStream_t>(stream));

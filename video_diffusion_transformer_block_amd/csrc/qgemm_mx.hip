@@ -566,7 +566,8 @@ hipError_t launch_qgemm_mx_grouped_256(bool a_fp8, const MxGrouped& q, hipStream
   // the device-side staged_store_ok, for every expert's bias and rows
   const bool staged = !p.out_f32 && (p.N % 8) == 0 && (p.ldy % 8) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 &&
                       (!p.bias || (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0);
-  if (mx_quads(q.K)) {
+  const bool quads = mx_quads(q.K) && ((reinterpret_cast<uintptr_t>(q.a_s) | reinterpret_cast<uintptr_t>(q.w_s)) & 15u) == 0;
+  if (quads) {
     if (a_fp8) return staged ? launch_mx_grouped<true, true, true>(p, grid, st) : launch_mx_grouped<true, true, false>(p, grid, st);
     return staged ? launch_mx_grouped<false, true, true>(p, grid, st) : launch_mx_grouped<false, true, false>(p, grid, st);
   }
