@@ -479,7 +479,8 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  * Errors: VDTQ_EINVAL for a bad a_fmt or size, null or misaligned pointers,
  * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128, K > 2^24,
  * N >= 2^26, T > 2^30 or more output tiles than a launch holds (2^24 of 256
- * rows of an expert x 256 features; with MXFP8 and fp32 output 64 x 128).
+ * rows of an expert x 256 features; of 64 x 128 with MXFP8 and fp32 output or
+ * weights of an expert of 4 GB or more).
  */
 int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
                      const uint8_t* w_q_dev, const uint8_t* w_s_dev,

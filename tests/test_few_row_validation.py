@@ -103,6 +103,7 @@ def _grp(**kw):
     (dict(aq=ODD), L.EINVAL), (dict(off=ctypes.c_void_p(0x100002)), L.EINVAL), (dict(T=(1 << 30) + 1), L.EUNSUPPORTED),
     (dict(N=1 << 26, ldy=1 << 26), L.EUNSUPPORTED), (dict(T=1 << 30, N=4096, ldy=4096), L.EUNSUPPORTED),
     (dict(T=1 << 24, N=8192, ldy=8192, od=1), L.EUNSUPPORTED),
+    (dict(T=1 << 26, N=4096, ldy=4096, K=1 << 22), L.EUNSUPPORTED),
 ])
 def test_grouped_rejects(kw, code):
     assert _grp(**kw) == code

@@ -294,6 +294,28 @@ def test_scales_far_from_one(kind):
             assert_elementwise(values(V.qgemv_mx(ad, wd, None, "f32")), want, t, K, "f32", kind)
 
 
+def test_grouped_weights_of_4_gb():
+    """An expert whose codes reach past 32-bit offsets: its last features
+    have the values that they have as an expert of their own.  (Both sums are
+    exact up to fp32 and the instruction's cut, 3.4e-5 of the norm here; one
+    bf16 step, 2^-7, covers a rounding that falls the other way.)"""
+    need_gpu()
+    K, N, T = 1 << 18, 32800, 200
+    assert N * K // 2 >= 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = V.MXTensor(torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+                   torch.randint(120, 124, (N, K // 32), dtype=torch.uint8, device="cuda", generator=g), "mxfp4")
+    a = V.hadamard_quantize((torch.randn(T, K, device="cuda", generator=g)).bfloat16(), 64, "mxfp8")
+    off = dev(np.array([0, T], np.int32))
+    y = V.qgemm_mx_grouped(a, w, off).float()
+    for lo, hi in ((0, 70), (N - 90, N)):
+        part = V.MXTensor(w.q[lo:hi].contiguous(), w.scales[lo:hi].contiguous(), "mxfp4")
+        z = V.qgemm_mx_grouped(a, part, off).float()
+        torch.cuda.synchronize()
+        tol = 2.0 ** -7 * z.abs() + 40 * 3.4e-5 * z.pow(2).mean().sqrt()
+        assert ((y[:, lo:hi] - z).abs() <= tol).all()
+
+
 def test_grouped_many_experts():
     need_gpu()
     c = rng_of(21).integers(0, 4, size=300).tolist()

@@ -407,8 +407,8 @@ int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, 
   if (!aligned(a_s_dev, 4) || !aligned(w_s_dev, 4)) return fail(VDTQ_EINVAL, "%s: scales need 4 bytes alignment", name);
   if (K % 128) return fail(VDTQ_EUNSUPPORTED, "%s: K=%lld is not a multiple of 128", name, (long long)K);
   if (T > (1 << 30)) return fail(VDTQ_EUNSUPPORTED, "%s: T=%lld is above 2^30", name, (long long)T);
-  const bool exact = a_fmt == VDTQ_FMT_MXFP8 && out_dtype == VDTQ_OUT_F32;
-  if (!vdtq::grouped_tiles_fit(T, E, N, exact ? 64 : 256, exact ? 128 : 256))
+  const bool small = (a_fmt == VDTQ_FMT_MXFP8 && out_dtype == VDTQ_OUT_F32) || !vdtq::grouped_256_fits(N, K);
+  if (!vdtq::grouped_tiles_fit(T, E, N, small ? 64 : 256, small ? 128 : 256))
     return fail(VDTQ_EUNSUPPORTED, "%s: too many output tiles", name);
   const vdtq::MxGrouped q{a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, offsets_dev, y_dev, ldy,
                           (int32_t)T, (int32_t)N, (int32_t)K, (int32_t)E, out_dtype == VDTQ_OUT_F32};

@@ -68,13 +68,9 @@ hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t
                         const float* w_ts, const float* bias, void* y, int64_t ldy, int out_dtype, int64_t M,
                         int64_t N, int64_t K, hipStream_t st);
 
-// Lets a kernel use `bytes` of dynamic LDS on the current device.
-inline hipError_t allow_lds(const void* kernel, int bytes) {
-  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-// allow_lds once per device and kernel (ID tells a file's kernels apart): the
-// call takes as long as a launch.  Two threads may both do it, with the same
+// Lets a kernel use `bytes` of dynamic LDS on the current device, once per
+// device and kernel (ID tells a file's kernels apart): the runtime's call
+// takes host time of its own.  Two threads may both do it, with the same
 // effect.
 template <int ID>
 static hipError_t allow_lds_once(const void* kernel, int bytes) {
@@ -83,7 +79,7 @@ static hipError_t allow_lds_once(const void* kernel, int bytes) {
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return hipSuccess;
-  e = allow_lds(kernel, bytes);
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   return e;
 }
@@ -101,6 +97,9 @@ struct MxGrouped {
   int32_t T, N, K, E;
   int32_t out_f32;
 };
+// Whether tiles of 256 x 256 can be used: they reach an expert's weights by
+// 32-bit offsets.
+inline bool grouped_256_fits(int64_t N, int64_t K) { return N * (K / 2) < (int64_t(1) << 32); }
 // Whether a launch can hold the tiles of bm rows x bn features (of 256
 // threads; a launch counts its threads in 32 bits).
 inline bool grouped_tiles_fit(int64_t T, int64_t E, int64_t N, int bm, int bn) {

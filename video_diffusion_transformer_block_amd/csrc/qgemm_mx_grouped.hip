@@ -1,18 +1,22 @@
 // MX products of rows grouped by expert (gfx950): the choice of a kernel, and
-// the one for experts of few rows.
+// those for experts of few and of middling row counts.
 //
 // Y[t] = A[t] W[e(t)]^T + bias[e(t)], the operands and the block-scaled matrix
 // instruction of qgemm_mx.hip.  With few rows an expert the time is that of
 // reading its weights once.
 //
-// A workgroup owns a tile of 16 rows of one expert and `tiles` blocks of 16 features one after the other.  Its wavefronts split K, 512
-// elements each: a wavefront keeps its part of the rows in registers as
-// operands of v_mfma_scale_f32_16x16x128_f8f6f4 and streams its part of the
-// weights through a ring of D blocks in LDS of its own by direct-to-LDS loads
-// (whole runs of rows; nothing is decoded, and no barrier is needed before
-// reading).  The sums of a block meet in LDS in wavefront order, one barrier
-// a block; the bias of all the workgroup's features is in LDS from the start,
-// because waiting for a load would wait for the ring's loads before it.
+// A workgroup owns a tile of 16 rows of one expert and `tiles` blocks of 16
+// features, one after the other.  Its wavefronts split K, 512 elements each
+// (1024 in two turns above K = 7168): a wavefront keeps its part of the rows in
+// registers as operands of v_mfma_scale_f32_16x16x128_f8f6f4 and streams its
+// part of the weights through a ring of D blocks in LDS of its own by
+// direct-to-LDS loads (whole runs of rows; nothing is decoded, and no barrier
+// is needed before reading).  The sums of a block meet in LDS in wavefront
+// order, one barrier a block; the bias of all the workgroup's features is in
+// LDS from the start, because waiting for a load would wait for the ring's
+// loads before it.  64 rows over 32 experts, 1920 -> 7680: 42 us, 4.7 TB/s of
+// the weights of the 25 experts hit (a copy reaches 5.2); decoding the operands
+// to bf16 and keeping the rows in LDS took 52.
 #include <algorithm>
 
 #include "device_common.h"
@@ -34,7 +38,7 @@ constexpr int kMgLoads = kMgCodes / 1024 + 1;
 constexpr uint32_t kMgNone = 0xFFFFFFF0u;       // an offset past every buffer: reads zeros
 
 constexpr int kMgRows = 16;
-constexpr int D = 2;                            // blocks of the ring (3 and 4: 8 % and 10 % slower, fewer workgroups fit)
+constexpr int D = 2;                            // blocks of the ring; with 3 or 4 fewer workgroups fit (8 - 10 % slower)
 constexpr int kMgMaxLds = 160 * 1024;
 
 struct MgParams {
@@ -230,6 +234,10 @@ struct MgTile {
   static constexpr int WGS = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;   // workgroups of a compute unit
 };
 
+// 1111 rows over 16 experts, 3072 -> 1920, MXFP8: 21 us for 58 MB and 13 GFLOP
+// (tiles of 256 x 256 took 41, of 128 x 128 26); what bounds it is the depth of
+// one tile (24 stages and the first loads' latency) with about 1.5 tiles a
+// workgroup slot.
 //
 // EXACT (MXFP8 rows, fp32 output): the fragments are decoded to bf16 (every
 // element times its block's power of two is exact) for
@@ -513,7 +521,8 @@ hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t s
     if (few) return launch_qgemm_mx_grouped_exact(q, st);
     return launch_tile<true, 64, 128, 2, true>(q, st);
   }
-  if (avg >= 192 || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)) return launch_qgemm_mx_grouped_256(a_fp8, q, st);
+  if (grouped_256_fits(q.N, q.K) && (avg >= 192 || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)))
+    return launch_qgemm_mx_grouped_256(a_fp8, q, st);
   if (few && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
   // three stages where three workgroups still fit a compute unit
   return a_fp8 ? launch_tile<true, 64, 128, 2>(q, st) : launch_tile<false, 64, 128, 3>(q, st);
