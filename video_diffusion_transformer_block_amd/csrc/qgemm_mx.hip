@@ -56,6 +56,7 @@
 #include "launch.h"
 #include "lds_dma.h"
 #include "qgemm_common.h"
+#include "ragged_store.h"
 #include "row_groups.h"
 
 namespace vdtq {
@@ -439,6 +440,61 @@ void qgemm_mx_kernel(GemmParams p) {
   }
   // epilogue: tile (i, j), lane, register e -> token row m0 + wm*128 + 32 i
   // + lane%32, feature column n0 + wn*128 + 32 j + 8 (e/4) + 4 (lane/32) + e%4
+  if constexpr (GROUPED) {
+    __syncthreads();   // every wave is past its last read of the ring
+    const int row0 = m0 + wm * 128, col0 = n0 + wn * 128;
+    if (p.out_f32) {
+      float* const l = reinterpret_cast<float*>(smem) + wv * (32 * 128);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            ragged_put<128>(l, r32, 32 * j + 8 * g + 4 * h, acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                            acc[i][j][4 * g + 3]);
+        ragged_store_f32<128>(l, static_cast<float*>(p.y) + (int64_t)(row0 + 32 * i) * p.ldy + col0, p.ldy,
+                              p.bias ? p.bias + col0 : nullptr, p.M - row0 - 32 * i, p.N - col0);
+      }
+      return;
+    }
+    // as stage_store_tile in two rounds, with the bias from LDS
+    float* const lb = reinterpret_cast<float*>(smem + 65536);
+    if (p.bias) lb[t] = p.bias[min(n0 + t, p.N - 1)];
+    __syncthreads();
+    uint8_t* const reg = smem + wv * 16384;
+#pragma unroll
+    for (int rd = 0; rd < 2; ++rd) {
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii) {
+        const int i = 2 * rd + ii, lrow = 32 * ii + r32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            if (p.bias) {
+              const float4 bb = *reinterpret_cast<const float4*>(lb + wn * 128 + 32 * j + 8 * g + 4 * h);
+              v[0] = v[0] + bb.x; v[1] = v[1] + bb.y; v[2] = v[2] + bb.z; v[3] = v[3] + bb.w;
+            }
+            *reinterpret_cast<uint2*>(reg + lrow * 256 + 16 * ((4 * j + g) ^ (lrow & 15)) + 8 * h) =
+                make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+          }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int c = lane & 15, n = p.N - col0 - 8 * c;
+#pragma unroll 4
+      for (int it = 0; it < 16; ++it) {
+        const int lrow = 4 * it + (lane >> 4), row = row0 + 64 * rd + lrow;
+        const uint4 w = *reinterpret_cast<const uint4*>(reg + lrow * 256 + 16 * (c ^ (lrow & 15)));
+        if (row < p.M) ragged_store8(static_cast<uint16_t*>(p.y) + (int64_t)row * p.ldy + col0 + 8 * c, w, n);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
+  }
   const bool vec = out_vec_ok(p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

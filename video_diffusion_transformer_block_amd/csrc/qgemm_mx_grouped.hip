@@ -23,6 +23,7 @@
 #include "launch.h"
 #include "lds_dma.h"
 #include "qgemm_common.h"
+#include "ragged_store.h"
 #include "row_groups.h"
 
 namespace vdtq {
@@ -231,6 +232,7 @@ struct MgTile {
   static constexpr int OUTROW = BN + 16;                           // bytes of a wavefront's output row in LDS
   static constexpr int OUT = 4 * (BM / 2) * OUTROW;
   static constexpr int LDS = MAIN > OUT ? MAIN : OUT;
+  static_assert(LDS >= 4 * 32 * (BN / 2) * 4 && LDS >= OUT + 4 * BN, "the epilogue's blocks and bias");
   static constexpr int WGS = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;   // workgroups of a compute unit
 };
 
@@ -425,38 +427,29 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   const int mrow = row0 + wm * (BM / 2), mleft = rows - wm * (BM / 2);
   const int ncol = n0 + wn * (BN / 2), nleft = feats - wn * (BN / 2);
   const float* const bias = p.bias ? p.bias + (int64_t)t.expert * N + n0 : nullptr;
-  auto biased = [&](int i, int j, int q, float (&v)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = acc[i][j][4 * q + e];
-      if (bias) v[e] = v[e] + bias[min(wn * (BN / 2) + 32 * j + 8 * q + 4 * h + e, feats - 1)];
-    }
-  };
+  wait_lgkm_barrier();                          // all are done with the ring
   if (p.out_f32) {
-    const bool whole4 = N % 4 == 0 && p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
+    float* const l = reinterpret_cast<float*>(mg_lds) + wv * 32 * (BN / 2);
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i)
+    for (int i = 0; i < S::TM; ++i) {
 #pragma unroll
       for (int j = 0; j < S::TN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[4];
-          biased(i, j, q, v);
-          const int r = 32 * i + r32, c = 32 * j + 8 * q + 4 * h;
-          if (r >= mleft) continue;
-          float* const y = static_cast<float*>(p.y) + (int64_t)(mrow + r) * p.ldy + ncol + c;
-          if (whole4 && c < nleft) {
-            *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c + e < nleft) y[e] = v[e];
-          }
-        }
+        for (int q = 0; q < 4; ++q)
+          ragged_put<BN / 2>(l, r32, 32 * j + 8 * q + 4 * h, acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                             acc[i][j][4 * q + 3]);
+      ragged_store_f32<BN / 2>(l, static_cast<float*>(p.y) + (int64_t)(mrow + 32 * i) * p.ldy + ncol, p.ldy,
+                               bias ? bias + wn * (BN / 2) : nullptr, mleft - 32 * i, nleft);
+    }
     return;
   }
-  // bf16: through LDS, so that a row's features leave in whole 16-byte pieces
-  wait_lgkm_barrier();                          // all are done with the ring
+  // bf16: through LDS, so that a row's features leave in 16-byte pieces; the
+  // bias comes from there too
+  float* const lb = reinterpret_cast<float*>(mg_lds + S::OUT);
+  if (bias) {
+    if (threadIdx.x < BN) lb[threadIdx.x] = bias[min((int)threadIdx.x, feats - 1)];
+    wait_lgkm_barrier();
+  }
   uint8_t* const out = mg_lds + wv * (BM / 2) * S::OUTROW;
 #pragma unroll
   for (int i = 0; i < S::TM; ++i)
@@ -464,8 +457,11 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
     for (int j = 0; j < S::TN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float v[4];
-        biased(i, j, q, v);
+        float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (bias) {
+          const float4 b = *reinterpret_cast<const float4*>(lb + wn * (BN / 2) + 32 * j + 8 * q + 4 * h);
+          v[0] = v[0] + b.x; v[1] = v[1] + b.y; v[2] = v[2] + b.z; v[3] = v[3] + b.w;
+        }
         *reinterpret_cast<uint2*>(out + (32 * i + r32) * S::OUTROW + 2 * (32 * j + 8 * q + 4 * h)) =
             make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
       }
@@ -473,21 +469,11 @@ __global__ __launch_bounds__(256, WGS) void mx_tile_kernel(MxGrouped p) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   constexpr int PPR = BN / 16;                  // 16-byte pieces of a row
-  const bool whole = N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
 #pragma unroll
   for (int it = 0; it < (BM / 2) * PPR / 64; ++it) {
     const int r = it * (64 / PPR) + lane / PPR, c = 8 * (lane % PPR);
     const uint4 v = *reinterpret_cast<const uint4*>(out + r * S::OUTROW + 2 * c);
-    if (r >= mleft || c >= nleft) continue;
-    uint16_t* const y = static_cast<uint16_t*>(p.y) + (int64_t)(mrow + r) * p.ldy + ncol + c;
-    if (whole) {
-      *reinterpret_cast<uint4*>(y) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < nleft) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
+    if (r < mleft) ragged_store8(static_cast<uint16_t*>(p.y) + (int64_t)(mrow + r) * p.ldy + ncol + c, v, nleft - c);
   }
 }
 

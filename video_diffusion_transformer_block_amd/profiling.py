@@ -37,7 +37,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # longer describe the kernels
 KERNEL_SOURCES = ["csrc/qgemm.hip", "csrc/qgemm_mx.hip", "csrc/qgemm_w4a16.hip", "csrc/hadamard_quantize.hip",
                   "csrc/block_stats.hip", "csrc/bench_stream.hip", "csrc/qgemm_common.h", "csrc/hadamard_common.h",
-                  "csrc/device_common.h", "csrc/lds_dma.h", "csrc/launch.h", "csrc/row_groups.h"]
+                  "csrc/device_common.h", "csrc/lds_dma.h", "csrc/launch.h", "csrc/row_groups.h",
+                  "csrc/ragged_store.h"]
 
 
 def source_hash() -> str:
