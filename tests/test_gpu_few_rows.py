@@ -597,3 +597,14 @@ def test_chain_in_graphs_and_on_two_streams():
         torch.cuda.synchronize()
         for k in (0, 1):
             assert all(torch.equal(a, b) for a, b in zip(got[k], want[k]))
+
+
+@pytest.mark.parametrize("afmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("counts,N,K", [
+    ([130, 126], 12288, 256), ([100, 0, 28], 9216, 128), ([400, 368], 1024, 512), ([1500, 4], 264, 128),
+    ([3, 2200, 0, 41], 1000, 256), ([14, 13, 12, 20], 8200, 128)])
+def test_grouped_where_either_tile_may_serve(afmt, counts, N, K):
+    """Counts and sizes on both sides of the choice between the two tile
+    sizes."""
+    need_gpu()
+    check_grouped(afmt, counts, N, K, front=1, back=2)

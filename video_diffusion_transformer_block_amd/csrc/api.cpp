@@ -343,8 +343,8 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
   return VDTQ_OK;
 }
 
-// The further checks of the few-row products.  With K a multiple of 128 the
-// scales are read as 8-byte (NVFP4) or 4-byte (MX) runs, else byte by byte.
+// The further checks of the few-row products.  With K a multiple of 128 every
+// row's scales start on 8 (NVFP4) or 4 bytes (MX) if the first ones do.
 static int gemv_check(const char* name, int64_t M, int64_t K, const void* w_s, const void* a_s, int run) {
   if (M > VDTQ_GEMV_MAX_ROWS)
     return fail(VDTQ_EUNSUPPORTED, "%s: M=%lld is more than %d rows", name, (long long)M, VDTQ_GEMV_MAX_ROWS);

@@ -18,6 +18,7 @@
 // the weights of the 25 experts hit (a copy reaches 5.2); decoding the operands
 // to bf16 and keeping the rows in LDS took 52.
 #include <algorithm>
+#include <cmath>
 
 #include "device_common.h"
 #include "launch.h"
@@ -236,7 +237,7 @@ struct MgTile {
   static constexpr int WGS = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;   // workgroups of a compute unit
 };
 
-// 1111 rows over 16 experts, 3072 -> 1920, MXFP8: 21 us for 58 MB and 13 GFLOP
+// 1111 rows over 16 experts, 3072 -> 1920, MXFP8: 20 us for 58 MB and 13 GFLOP
 // (tiles of 256 x 256 took 41, of 128 x 128 26); what bounds it is the depth of
 // one tile (24 stages and the first loads' latency) with about 1.5 tiles a
 // workgroup slot.
@@ -488,28 +489,49 @@ static hipError_t launch_tile(const MxGrouped& q, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Whether 256 x 256 tiles are the faster ones, from what was measured of both
+// (us, K in thousands, per round of one tile a compute unit): a 256 x 256
+// tile takes 9 + 11.4 K (MXFP8 rows; 9 + 8 K MXFP4) and whole rounds count; a
+// 64 x 128 tile 2.95 K (2.35 K) and fractions of a round count, three share a
+// unit, and 8 for the first.  The counts are on the device, so half a tile of
+// rows an expert is taken as empty, and a round that this fills is taken to
+// spill into another.  Both, MXFP8 rows, skewed counts:
+//   N x K x experts      128 rows (64 x 128, 256 x 256)
+//                                             192        384         768         2200
+//   1920 x 3072 x 16     29  42               39  43     63  84      114  93     285  234
+//   7680 x 1920 x 8      32  36               50  65     85  71      147  131    369  296
+//   12288 x 3072 x 4     46  44               58  45     93  86      169  134    436  314
+//   3072 x 12288 x 8     87  149              110 155    185 163     343  299    927  656
+//   1024 x 512 x 32      10  15               15  15     21  28      33   30     96   70
+static bool tiles_256_faster(bool a_fp8, const MxGrouped& q) {
+  const double k = q.K * 1e-3, cus = device_cu_count();
+  const double t256 = ((double)q.T / 256 + 0.5 * q.E) * ((q.N + 255) / 256);
+  const double t64 = ((double)q.T / 64 + 0.5 * q.E) * ((q.N + 127) / 128);
+  return (std::floor(t256 / cus) + 1) * (9 + (a_fp8 ? 11.4 : 8.0) * k) < 8 + t64 / cus * (a_fp8 ? 2.95 : 2.35) * k;
+}
+
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st) {
-  // By the average rows of an expert (their counts are on the device), both
-  // sides of each border measured with skewed counts, MXFP8, us:
-  //   N x K x experts     8 rows            16                32       128              256
-  //   1920 x 3072 x 16    stream 16, 64: 19 stream 20, 64: 19 28, 19   64: 31, 256: 44  64: 49, 256: 46
-  //   7680 x 1920 x 8     17, 19            20, 19            23, 19   36, 38           69, 69
-  //   3072 x 12288 x 8    41, 57            55, 57            80, 60   88, 150          -
+  // By the average rows of an expert (their counts are on the device).  The
+  // few-row kernel against 64 x 128 tiles, skewed counts, MXFP8, us:
+  //   N x K x experts     8 rows    16        32
+  //   1920 x 3072 x 16    16  17    19  17    25  18
+  //   7680 x 1920 x 8     17  16    19  16    30  17
+  //   3072 x 12288 x 8    42  57    55  58    80  59
   const int avg = q.T / q.E;
   // the few-row kernels count row tiles in the launch's y, which ends at 2^16
   const bool few = avg <= 12 && q.T / 16 + q.E < 65536;
   // fp32 output of MXFP8 rows: sums of exact products, which the block-scaled
-  // instruction does not form.  8 rows an expert: 17 us by the few-row kernel,
-  // 27 by tiles (1920 x 3072 x 16), 58 and 78 (3072 x 12288 x 8); 16 rows: 28
-  // and 27, 87 and 80; tiles of 128 x 128 are 8 % faster at thousands of rows,
-  // 40 % slower below 64
+  // instruction does not form.  The few-row kernel against tiles, 8 rows an
+  // expert: 17 and 24 us (1920 x 3072 x 16), 31 and 24 (7680 x 1920 x 8), 58 and
+  // 75 (3072 x 12288 x 8); 16 rows: 25 and 25, 32 and 24, 60 and 77; tiles of
+  // 128 x 128 are 8 % faster at thousands of rows, 40 % slower below 64
   if (a_fp8 && q.out_f32) {
     if (few) return launch_qgemm_mx_grouped_exact(q, st);
     return launch_tile<true, 64, 128, 2, true>(q, st);
   }
-  if (grouped_256_fits(q.N, q.K) && (avg >= 192 || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)))
-    return launch_qgemm_mx_grouped_256(a_fp8, q, st);
   if (few && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
+  if (grouped_256_fits(q.N, q.K) && (tiles_256_faster(a_fp8, q) || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)))
+    return launch_qgemm_mx_grouped_256(a_fp8, q, st);
   // three stages where three workgroups still fit a compute unit
   return a_fp8 ? launch_tile<true, 64, 128, 2>(q, st) : launch_tile<false, 64, 128, 3>(q, st);
 }

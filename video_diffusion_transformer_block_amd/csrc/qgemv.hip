@@ -212,7 +212,7 @@ __device__ __forceinline__ gv_uint2 load_scales(const uint8_t* base, int rows, i
       typedef uint16_t u0 __attribute__((aligned(1)));
       d[0] = *reinterpret_cast<const u0*>(p);
     }
-  } else {
+  } else if (k < K) {
 #pragma unroll
     for (int b = 0; b < SB; ++b)
       if (k + G * b < K) d[b >> 2] |= (uint32_t)p[b] << (8 * (b & 3));
