@@ -15,7 +15,7 @@
 //
 // Bound: memory.  17776 x 3072 with residual, MXFP8 out, moves 384 MB in 70.6
 // us (5.4 TB/s; a plain copy of 1 GB reaches 5.2 on the same card); the vector
-// unit is busy for about 40 us of it.
+// units are busy for two thirds of it.
 //
 // Layout: T lanes own a row (T = 8, 16, 64, 128 or 256), each holding C vectors
 // of 8 consecutive elements, vector c of lane t at element 8 (c T + t): every
