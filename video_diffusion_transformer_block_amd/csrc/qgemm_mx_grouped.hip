@@ -179,14 +179,17 @@ __global__ __launch_bounds__(64 * kMgMaxWaves) void mx_stream_kernel(MgParams mp
 
 template <bool A8, int TURNS>
 static hipError_t launch_stream(const MxGrouped& q, int nw, hipStream_t st) {
-  // feature blocks of a workgroup: up to 8, as long as every compute unit has
-  // two workgroups (4 or 16 of them: within 10 %)
-  const int blocks = (q.N + 15) / 16;
-  const int64_t wgs = (int64_t)blocks * std::min(q.E, q.T);
-  const MgParams p{q, (int)std::max<int64_t>(1, std::min<int64_t>(8, wgs / (2 * device_cu_count())))};
+  // feature blocks of a workgroup: so many that all workgroups run at once, up
+  // to 8 (16: 5 - 30 % slower).  2 workgroups a unit whatever their LDS took
+  // 20.2 us against 12.1 for 12 rows over 3 experts (K = 5504, N = 4561), 28.8
+  // against 12.4 for 2 over 20 (4992, 4619), 16.1 against 14.3 for 128 over 16
+  // (3072, 1920)
+  const int blocks = (q.N + 15) / 16, wave = 2 * 1024 + D * kMgSlot;
+  const int64_t wgs = (int64_t)blocks * std::min(q.E, q.T), slots = (int64_t)device_cu_count() * (kMgMaxLds / (nw * wave));
+  const MgParams p{q, (int)std::min<int64_t>(8, (wgs + slots - 1) / slots)};
   const hipError_t e = allow_lds_once<A8 * 2 + TURNS - 1>(reinterpret_cast<const void*>(&mx_stream_kernel<A8, TURNS>), kMgMaxLds);
   if (e != hipSuccess) return e;
-  const int lds = nw * (2 * 1024 + D * kMgSlot) + 64 * p.tiles;
+  const int lds = nw * wave + 64 * p.tiles;
   hipLaunchKernelGGL((mx_stream_kernel<A8, TURNS>), dim3((unsigned)((blocks + p.tiles - 1) / p.tiles), (unsigned)(q.T / kMgRows + q.E)),
                      dim3(64 * nw), lds, st, p);
   return hipGetLastError();

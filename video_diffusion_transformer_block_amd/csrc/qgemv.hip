@@ -64,7 +64,6 @@ struct GemvParams {
   int64_t ldy;
   int32_t M, N, K, E;
   int32_t out_f32;
-  int32_t tiles;             // feature tiles of a workgroup
 };
 
 // One operand of the matrix instruction, 8 values: fp16 for INT8
@@ -250,7 +249,9 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
   uint8_t* const lw = gv_lds + nw * 1024 * MT + wv * S::LDS;
   uint8_t* const la = lw + 16 * S::WROW;
 
-  const int tile0 = blockIdx.x * p.tiles, tiles = min(p.tiles, (p.N + 15) / 16 - tile0);
+  const int n0 = blockIdx.x * 16, nr = min(16, p.N - n0);
+  const int64_t row0 = expert * p.N + n0;
+  const __amdgpu_buffer_rsrc_t wq = raw_buffer(p.w_q + row0 * wrow, nr * wrow);
   const int steps = (K + KS - 1) / KS;
   const int turns = (steps - wv + nw - 1) / nw;          // of this wavefront, at least one
 
@@ -259,11 +260,12 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
   uint32_t ra[MT], fa[MT];                      // MX, not decoded: scales as loaded, and of this lane's pieces
   gv_uint2 sw, fs;                              // weight scales as loaded, and of this lane's pieces
   float4v acc[MT];
-  // iteration it: the codes of the one before go to LDS, its own are loaded,
-  // the ones in LDS are multiplied
-  int tile = 0, turn = 0, ptile = 0, pturn = 0;
-  for (bool first = true;; first = false) {
-    if (!first) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
+  // a turn: the codes of the one before go to LDS, its own are loaded, the
+  // ones in LDS are multiplied
+  for (int turn = 0;; ++turn) {
+    if (turn > 0) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
 #pragma unroll
       for (int i = 0; i < S::WLOADS; ++i) {
@@ -272,35 +274,29 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
       }
       fs[0] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sw[0]);
       if constexpr (S::SB == 8) fs[1] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), sw[1]);
-      if (turns > 1 || ptile == 0) {
 #pragma unroll
-        for (int i = 0; i < S::ALOADS; ++i) {
-          const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
-          if constexpr (!S::DECODED) {
-            *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * ((lane % (S::AROW / 16)) ^ (row & 7))) = ca[i];
-          } else if (MR * S::AROW >= 1024 || row < MR) {
+      for (int i = 0; i < S::ALOADS; ++i) {
+        const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
+        if constexpr (!S::DECODED) {
+          *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * ((lane % (S::AROW / 16)) ^ (row & 7))) = ca[i];
+        } else if (MR * S::AROW >= 1024 || row < MR) {
 #pragma unroll
-            for (int j = 0; j < E / 8; ++j) {
-              const GvFrag<AF> d = decode_act<AF>(ca[i], MX ? e8m0(sa[i]) : 0.0f, j);
-              const int piece = lane % (S::AROW / 16) * (E / 8) + j;
-              *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * (piece ^ (row & 7))) = make_uint4(d.w[0], d.w[1], d.w[2], d.w[3]);
-            }
+          for (int j = 0; j < E / 8; ++j) {
+            const GvFrag<AF> d = decode_act<AF>(ca[i], MX ? e8m0(sa[i]) : 0.0f, j);
+            const int piece = lane % (S::AROW / 16) * (E / 8) + j;
+            *reinterpret_cast<uint4*>(la + row * S::DROW + 16 * (piece ^ (row & 7))) = make_uint4(d.w[0], d.w[1], d.w[2], d.w[3]);
           }
         }
-        if constexpr (MX && !S::DECODED) {
+      }
+      if constexpr (MX && !S::DECODED) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) fa[i] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), ra[i]);
-        }
+        for (int i = 0; i < MT; ++i) fa[i] = __builtin_amdgcn_ds_bpermute(4 * (4 * r + g), ra[i]);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
-    if (tile < tiles) {
+    if (turn < turns) {
       const int k0 = (turn * nw + wv) * KS;
-      const int n0 = (tile0 + tile) * 16;
-      const int64_t row0 = expert * p.N + n0;
-      const int nr = min(16, p.N - n0);
-      const __amdgpu_buffer_rsrc_t wq = raw_buffer(p.w_q + row0 * wrow, nr * wrow);
 #pragma unroll
       for (int i = 0; i < S::WLOADS; ++i) {
         const int row = i * (1024 / S::WROW) + lane / (S::WROW / 16);
@@ -317,27 +313,20 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
       }
       const int ks = k0 + (lane & 3) * (KS / 4);
       sw = load_scales<S::SB, G>(p.w_s + row0 * srow, nr, lane >> 2, srow, ks, K);
-      // with one turn the activations of the first tile serve all
-      if (turns > 1 || tile == 0) {
 #pragma unroll
-        for (int i = 0; i < S::ALOADS; ++i) {
-          const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
-          const int k = k0 + E * (lane % (S::AROW / 16));
-          ca[i] = buffer_load16(aq, k < K ? row * arow + (uint32_t)k / 32 * ActBytes<AF>::n + (uint32_t)k % 32 * ActBytes<AF>::n / 32 : kGvNone);
-          if constexpr (MX && S::DECODED)
-            sa[i] = __builtin_amdgcn_raw_buffer_load_b8(as, k < K ? row * srow + k / 32 : kGvNone, 0, 0);
-        }
-        if constexpr (MX && !S::DECODED) {
+      for (int i = 0; i < S::ALOADS; ++i) {
+        const int row = i * S::ALOAD_ROWS + lane / (S::AROW / 16);
+        const int k = k0 + E * (lane % (S::AROW / 16));
+        ca[i] = buffer_load16(aq, k < K ? row * arow + (uint32_t)k / 32 * ActBytes<AF>::n + (uint32_t)k % 32 * ActBytes<AF>::n / 32 : kGvNone);
+        if constexpr (MX && S::DECODED)
+          sa[i] = __builtin_amdgcn_raw_buffer_load_b8(as, k < K ? row * srow + k / 32 : kGvNone, 0, 0);
+      }
+      if constexpr (MX && !S::DECODED) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) ra[i] = load_scales<S::SB, G>(asp, rows, 16 * i + (lane >> 2), srow, ks, K)[0];
-        }
+        for (int i = 0; i < MT; ++i) ra[i] = load_scales<S::SB, G>(asp, rows, 16 * i + (lane >> 2), srow, ks, K)[0];
       }
     }
-    if (!first) {
-      if (pturn == 0) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
-      }
+    if (turn > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int piece = U * g + u;            // 32 elements of the step
@@ -375,66 +364,58 @@ __global__ __launch_bounds__(MR == 32 ? 512 : 1024) void qgemv_kernel(GemvParams
         }
       }
     }
-    if (!first && pturn == turns - 1) {
-      // register e of lane l: row 4 (l / 16) + e, feature l % 16
+    if (turn == turns) break;
+  }
+  // register e of lane l: row 4 (l / 16) + e, feature l % 16
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[(wv * 16 * MT + 16 * i + 4 * g + e) * 16 + r] = acc[i][e];
-      wait_lgkm_barrier();                      // leaves the loads in flight
-      const int n0 = (tile0 + ptile) * 16;
-      for (int o = threadIdx.x; o < 256 * MT; o += blockDim.x) {
-        const int mr = o >> 4, nc = o & 15;
-        if (mr >= rows || n0 + nc >= p.N) continue;
-        float s = part[o];
-        for (int w = 1; w < nw; ++w) s = s + part[w * 256 * MT + o];
-        const int64_t m = m0 + mr;
-        if constexpr (AF == kActBf16) s = s * p.w_ts[1];
-        if constexpr (AF == kActInt8) s = s * (static_cast<const float*>(p.a_s)[m] * p.w_ts[1]);
-        if (p.bias) s = s + p.bias[expert * p.N + n0 + nc];
-        if (p.out_f32)
-          static_cast<float*>(p.y)[m * p.ldy + n0 + nc] = s;
-        else
-          static_cast<__bf16*>(p.y)[m * p.ldy + n0 + nc] = (__bf16)s;
-      }
-      if (ptile + 1 == tiles) return;
-      wait_lgkm_barrier();                      // the sums are read before the next tile's
-    }
-    ptile = tile;
-    pturn = turn;
-    if (++turn == turns) {
-      turn = 0;
-      ++tile;
-    }
+    for (int e = 0; e < 4; ++e) part[(wv * 16 * MT + 16 * i + 4 * g + e) * 16 + r] = acc[i][e];
+  __syncthreads();
+  for (int o = threadIdx.x; o < 256 * MT; o += blockDim.x) {
+    const int mr = o >> 4, nc = o & 15;
+    if (mr >= rows || nc >= nr) continue;
+    float s = part[o];
+    for (int w = 1; w < nw; ++w) s = s + part[w * 256 * MT + o];
+    const int64_t m = m0 + mr;
+    if constexpr (AF == kActBf16) s = s * p.w_ts[1];
+    if constexpr (AF == kActInt8) s = s * (static_cast<const float*>(p.a_s)[m] * p.w_ts[1]);
+    if (p.bias) s = s + p.bias[row0 + nc];
+    if (p.out_f32)
+      static_cast<float*>(p.y)[m * p.ldy + n0 + nc] = s;
+    else
+      static_cast<__bf16*>(p.y)[m * p.ldy + n0 + nc] = (__bf16)s;
   }
 }
 
+// `most_per_cu`: the workgroups of a compute unit that the LDS is shared out
+// to, if there are so many.
 template <int AF, int MR>
-static hipError_t launch_tiles(GemvParams p, int gy, int tiles, int64_t max_lds, hipStream_t st) {
+static hipError_t launch_rows(const GemvParams& p, int gy, int64_t wgs, int most_per_cu, hipStream_t st) {
   using S = GvStep<AF, MR>;
-  p.tiles = tiles;
-  // wavefronts: one per step of K while they fit, then evenly loaded ones
-  const int steps = (p.K + S::KS - 1) / S::KS, wave = S::LDS + 1024 * S::MT;
-  const int most = (int)std::min<int64_t>(S::WAVES, max_lds / wave);
-  const int turns = (steps + most - 1) / most, nw = (steps + turns - 1) / turns;
-  const hipError_t e = allow_lds_once<AF * 64 + MR>(reinterpret_cast<const void*>(&qgemv_kernel<AF, MR>), kGvMaxLds);
-  if (e != hipSuccess) return e;
-  const int64_t gx = ((p.N + 15) / 16 + tiles - 1) / tiles;
-  hipLaunchKernelGGL((qgemv_kernel<AF, MR>), dim3((unsigned)gx, (unsigned)gy), dim3(64 * nw), nw * wave, st, p);
-  return hipGetLastError();
-}
-
-template <int AF>
-static hipError_t launch_gemv(const GemvParams& p, hipStream_t st) {
   // LDS for all workgroups to run at once.  12288 features (3 workgroups a
   // compute unit), K = 3072: 8.8 us with 3 wavefronts of 2 turns against 10.2
   // with 6 of one (one INT8 row), 12.0 against 14.3 with 160 KB for two (32
   // MXFP8 rows); 3072 features, K = 12288 (one): 9.9 us with all of it, 10.5
   // with half (16 MXFP8 rows)
-  const int64_t per_cu = ((p.N + 15) / 16 + device_cu_count() - 1) / device_cu_count();
-  const int64_t lds = kGvMaxLds / std::min<int64_t>(per_cu, 4);
-  if (p.M <= 4) return launch_tiles<AF, 4>(p, 1, 1, lds, st);
-  return p.M <= 16 ? launch_tiles<AF, 16>(p, 1, 1, lds, st) : launch_tiles<AF, 32>(p, 1, 1, lds, st);
+  const int64_t per_cu = (wgs + device_cu_count() - 1) / device_cu_count();
+  const int64_t lds = kGvMaxLds / std::min<int64_t>(per_cu, most_per_cu);
+  // wavefronts: one per step of K while they fit, then evenly loaded ones
+  const int steps = (p.K + S::KS - 1) / S::KS, wave = S::LDS + 1024 * S::MT;
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>(S::WAVES, lds / wave));
+  const int turns = (steps + most - 1) / most, nw = (steps + turns - 1) / turns;
+  const hipError_t e = allow_lds_once<AF * 64 + MR>(reinterpret_cast<const void*>(&qgemv_kernel<AF, MR>), kGvMaxLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((qgemv_kernel<AF, MR>), dim3((unsigned)((p.N + 15) / 16), (unsigned)gy), dim3(64 * nw), nw * wave, st, p);
+  return hipGetLastError();
+}
+
+template <int AF>
+static hipError_t launch_gemv(const GemvParams& p, hipStream_t st) {
+  // 5 a unit: 18432 features, K = 3072, 16 MXFP8 rows: 11.7 us, 12.8 with 4
+  const int64_t wgs = (p.N + 15) / 16;
+  if (p.M <= 4) return launch_rows<AF, 4>(p, 1, wgs, 5, st);
+  return p.M <= 16 ? launch_rows<AF, 16>(p, 1, wgs, 5, st) : launch_rows<AF, 32>(p, 1, wgs, 5, st);
 }
 
 hipError_t launch_qgemv(int act, const void* a_q, const void* a_s, const uint8_t* w_q, const uint8_t* w_s,
@@ -460,8 +441,11 @@ hipError_t launch_qgemm_mx_grouped_exact(const MxGrouped& q, hipStream_t st) {
   p.w_q = q.w_q; p.w_s = q.w_s; p.bias = q.bias; p.offsets = q.offsets;
   p.y = q.y; p.ldy = q.ldy; p.out_f32 = q.out_f32;
   p.M = q.T; p.N = q.N; p.K = q.K; p.E = q.E;
-  // 4 feature tiles a workgroup: finding its rows takes about as long as one
-  return launch_tiles<kActMx8, 16>(p, q.T / 16 + q.E, 4, kGvMaxLds / 2, st);
+  // 8 a unit: 64 rows over 32 experts, K = 1920, N = 7680: 78 us, 94 with 4;
+  // half the LDS each and 4 feature tiles one after the other took 108 (2 rows
+  // over 20 experts, K = 4992, N = 4619: 13.4 and 21.8)
+  const int64_t wgs = (int64_t)((q.N + 15) / 16) * std::min(q.E, q.T);
+  return launch_rows<kActMx8, 16>(p, q.T / 16 + q.E, wgs, 8, st);
 }
 
 }  // namespace vdtq
