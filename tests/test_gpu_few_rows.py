@@ -608,3 +608,13 @@ def test_grouped_where_either_tile_may_serve(afmt, counts, N, K):
     sizes."""
     need_gpu()
     check_grouped(afmt, counts, N, K, front=1, back=2)
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([12, 13], 100, 512), ([15, 17], 4100, 256), ([16], 70, 1152), ([17], 70, 1152), ([5, 0, 7], 4561, 5504),
+    ([1, 0, 0, 1, 0, 0], 4619, 1280), ([9, 2], 40, 16384)])
+def test_grouped_few_rows_in_many_workgroups(counts, N, K):
+    """Both few-row kernels where a workgroup takes one, several or not all
+    feature blocks, and K of one and of many turns."""
+    need_gpu()
+    check_grouped("mxfp8", counts, N, K, front=1, back=1)

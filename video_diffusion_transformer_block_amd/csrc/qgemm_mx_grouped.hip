@@ -516,23 +516,25 @@ static bool tiles_256_faster(bool a_fp8, const MxGrouped& q) {
 hipError_t launch_qgemm_mx_grouped(bool a_fp8, const MxGrouped& q, hipStream_t st) {
   // By the average rows of an expert (their counts are on the device).  The
   // few-row kernel against 64 x 128 tiles, skewed counts, MXFP8, us:
-  //   N x K x experts     8 rows    16        32
-  //   1920 x 3072 x 16    16  17    19  17    25  18
-  //   7680 x 1920 x 8     17  16    19  16    30  17
-  //   3072 x 12288 x 8    42  57    55  58    80  59
+  //   N x K x experts     8 rows    12        16        32
+  //   1920 x 3072 x 16    14  17    15  17    21  17    28  18
+  //   7680 x 1920 x 8     15  16    17  16    18  16    26  17
+  //   3072 x 12288 x 8    37  57    48  57    52  60    64  58
+  //   4096 x 4096 x 16    40  35    42  38    42  40    61  41
+  //   1024 x 512 x 32     7   7     7   7     8   7     12  8
   const int avg = q.T / q.E;
   // the few-row kernels count row tiles in the launch's y, which ends at 2^16
-  const bool few = avg <= 12 && q.T / 16 + q.E < 65536;
+  const bool y_fits = q.T / 16 + q.E < 65536;
   // fp32 output of MXFP8 rows: sums of exact products, which the block-scaled
-  // instruction does not form.  The few-row kernel against tiles, 8 rows an
-  // expert: 17 and 24 us (1920 x 3072 x 16), 31 and 24 (7680 x 1920 x 8), 58 and
-  // 75 (3072 x 12288 x 8); 16 rows: 25 and 25, 32 and 24, 60 and 77; tiles of
-  // 128 x 128 are 8 % faster at thousands of rows, 40 % slower below 64
+  // instruction does not form.  The same five shapes, 8 rows: 17  24, 23  23,
+  // 45  77, 43  49, 7  9; 16 rows: 20  25, 27  24, 62  79, 52  51, 8  9; 20 rows:
+  // 25  25, 34  25, 72  78, 61  51, 11  10; tiles of 128 x 128 are 8 % faster at
+  // thousands of rows, 40 % slower below 64
   if (a_fp8 && q.out_f32) {
-    if (few) return launch_qgemm_mx_grouped_exact(q, st);
+    if (avg <= 16 && y_fits) return launch_qgemm_mx_grouped_exact(q, st);
     return launch_tile<true, 64, 128, 2, true>(q, st);
   }
-  if (few && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
+  if (avg <= 12 && y_fits && q.K <= 2 * kMgMaxWaves * kMgStep) return a_fp8 ? stream<true>(q, st) : stream<false>(q, st);
   if (grouped_256_fits(q.N, q.K) && (tiles_256_faster(a_fp8, q) || !grouped_tiles_fit(q.T, q.E, q.N, 64, 128)))
     return launch_qgemm_mx_grouped_256(a_fp8, q, st);
   // three stages where three workgroups still fit a compute unit

@@ -24,7 +24,7 @@
 // Loads: lane l of the matrix instruction holds feature (or row) l % 16, so
 // fragments read straight from memory touch 64 places of 16 bytes each, and a
 // compute unit looks up about one place a cycle (such a kernel took 17.9 us
-// for 32 bf16 rows, K = 1920, N = 7679, against 8.9 here).  Instead a wavefront
+// for 32 bf16 rows, K = 1920, N = 7679, against 8.1 here).  Instead a wavefront
 // reads whole runs of rows (1 KB an instruction), puts them into LDS of its own
 // (no barrier: its LDS operations run in order) and takes the fragments from
 // there; the next step's loads are in flight meanwhile.  Rows of 16-byte pieces are stored
@@ -33,7 +33,7 @@
 // resources: rows past M or N and elements past K read as zeros.
 //
 // Bound: latency.  A kernel that does nothing takes 4.2 us of a replayed
-// graph; 21 MB of weights (K = 3072, N = 12288, one row) take 8.8, of which the
+// graph; 21 MB of weights (K = 3072, N = 12288, one row) take 8.6, of which the
 // copy rate would account for 4.1: one round of loads, their pass through LDS
 // and the join follow each other, with the vector units busy 19 - 30 % of the
 // time and the matrix cores 3 - 6 %.
