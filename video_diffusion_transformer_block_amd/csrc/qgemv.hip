@@ -41,7 +41,6 @@
 
 #include "device_common.h"
 #include "launch.h"
-#include "lds_dma.h"
 #include "row_groups.h"
 
 namespace vdtq {
