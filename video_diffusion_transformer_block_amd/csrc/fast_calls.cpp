@@ -7,7 +7,9 @@
 // Every function returns None, with nothing launched, where anything is not
 // the ordinary case (another device than the current one, a strided or
 // subclassed tensor, a wrong type or shape, a size the library refuses): the
-// Python path in ops.py then does the call or raises its error.
+// Python path in ops.py then does the call or raises its error.  Any other
+// failure is answered with the library's status as an int, which the caller
+// raises: that call is not made again.
 #include <Python.h>
 
 #include <ATen/hip/EmptyTensor.h>
@@ -74,6 +76,13 @@ bool output(PyObject* y, int64_t M, int64_t N, int out, int dev, at::TensorBase&
   return true;
 }
 
+// What the Python caller makes of a status other than VDTQ_OK: a refusal
+// launches nothing, and the Python path names it.
+PyObject* failed(int rc) {
+  if (rc == VDTQ_EINVAL || rc == VDTQ_EUNSUPPORTED) Py_RETURN_NONE;
+  return PyLong_FromLong(rc);
+}
+
 PyObject* give(PyObject* y, at::TensorBase&& t) {
   if (is_none(y)) return THPVariable_Wrap(std::move(t));
   Py_INCREF(y);
@@ -120,7 +129,7 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   else
     rc = qgemv_mx(kind == kMx8 ? VDTQ_FMT_MXFP8 : VDTQ_FMT_MXFP4, static_cast<const uint8_t*>(ptr(aq)),
                   static_cast<const uint8_t*>(ptr(as)), wqp, wsp, bp, yp, N, out, M, N, K, stream(dev));
-  if (rc != VDTQ_OK) Py_RETURN_NONE;
+  if (rc != VDTQ_OK) return failed(rc);
   return give(a[7], std::move(y));
   END_HANDLE_TH_ERRORS
 }
@@ -153,7 +162,7 @@ PyObject* grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
       a8 ? VDTQ_FMT_MXFP8 : VDTQ_FMT_MXFP4, static_cast<const uint8_t*>(ptr(aq)), static_cast<const uint8_t*>(ptr(as)),
       static_cast<const uint8_t*>(ptr(wq)), static_cast<const uint8_t*>(ptr(ws)), static_cast<const float*>(ptr(bias)),
       static_cast<const int32_t*>(ptr(off)), E, y.mutable_data_ptr(), N, out, T, N, K, stream(dev));
-  if (rc != VDTQ_OK) Py_RETURN_NONE;
+  if (rc != VDTQ_OK) return failed(rc);
   return give(a[7], std::move(y));
   END_HANDLE_TH_ERRORS
 }
@@ -196,7 +205,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int rc = rmsnorm_quantize(ptr(x), M, K, K, ptr(res), K, static_cast<const float*>(ptr(w)), (float)eps, (int)b,
                                   (int)fmt, res ? sum.mutable_data_ptr() : nullptr, K, q.mutable_data_ptr(),
                                   scales.defined() ? scales.mutable_data_ptr() : nullptr, stream(dev));
-  if (rc != VDTQ_OK) Py_RETURN_NONE;
+  if (rc != VDTQ_OK) return failed(rc);
   PyObject* pq = THPVariable_Wrap(std::move(q));
   PyObject* ps = Py_None;
   PyObject* pr = Py_None;

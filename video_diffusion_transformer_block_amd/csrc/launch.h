@@ -84,6 +84,16 @@ static hipError_t allow_lds_once(const void* kernel, int bytes) {
   return e;
 }
 
+// Launches a kernel that takes one struct; the status is this launch's own.
+// (hipGetLastError after it would also give an error that other code left
+// pending on the thread, and take it from whoever looks for it, while the
+// kernel runs.)
+template <class P>
+static hipError_t launch_kernel(void (*kernel)(P), dim3 grid, dim3 block, unsigned lds, hipStream_t st, P p) {
+  void* args[] = {&p};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, lds, st);
+}
+
 // Rows grouped by expert (MX operands): the choice of a kernel
 // (qgemm_mx_grouped.hip) and the ones of other files it chooses between:
 // 256 x 256 tiles (qgemm_mx.hip), and sums of exact products of few MXFP8

@@ -520,8 +520,7 @@ static hipError_t launch_mx_grouped(const GemmParams& p, unsigned grid, hipStrea
   const int lds = MxPipe<A8, QUADS>::LDS;
   const hipError_t e = allow_lds_once<A8 * 4 + QUADS * 2 + STAGED>(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((qgemm_mx_kernel<A8, QUADS, false, STAGED, 0, true>), dim3(grid), dim3(GT), lds, st, p);
-  return hipGetLastError();
+  return launch_kernel(kernel, dim3(grid), dim3(GT), lds, st, p);
 }
 
 template <bool A8, bool QUADS, bool SPLIT, bool STAGED, int QOUT = 0>

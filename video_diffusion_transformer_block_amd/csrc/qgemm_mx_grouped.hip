@@ -190,9 +190,8 @@ static hipError_t launch_stream(const MxGrouped& q, int nw, hipStream_t st) {
   const hipError_t e = allow_lds_once<A8 * 2 + TURNS - 1>(reinterpret_cast<const void*>(&mx_stream_kernel<A8, TURNS>), kMgMaxLds);
   if (e != hipSuccess) return e;
   const int lds = nw * wave + 64 * p.tiles;
-  hipLaunchKernelGGL((mx_stream_kernel<A8, TURNS>), dim3((unsigned)((blocks + p.tiles - 1) / p.tiles), (unsigned)(q.T / kMgRows + q.E)),
-                     dim3(64 * nw), lds, st, p);
-  return hipGetLastError();
+  return launch_kernel(&mx_stream_kernel<A8, TURNS>,
+                       dim3((unsigned)((blocks + p.tiles - 1) / p.tiles), (unsigned)(q.T / kMgRows + q.E)), dim3(64 * nw), lds, st, p);
 }
 
 template <bool A8>
@@ -488,8 +487,7 @@ static hipError_t launch_tile(const MxGrouped& q, hipStream_t st) {
       reinterpret_cast<const void*>(&mx_tile_kernel<A8, BM, BN, NS, EXACT>), S::LDS);
   if (e != hipSuccess) return e;
   const int64_t grid = (int64_t)(q.T / BM + q.E) * ((q.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx_tile_kernel<A8, BM, BN, NS, EXACT>), dim3((unsigned)grid), dim3(256), S::LDS, st, q);
-  return hipGetLastError();
+  return launch_kernel(&mx_tile_kernel<A8, BM, BN, NS, EXACT>, dim3((unsigned)grid), dim3(256), S::LDS, st, q);
 }
 
 // Whether 256 x 256 tiles are the faster ones, from what was measured of both

@@ -405,8 +405,7 @@ static hipError_t launch_rows(const GemvParams& p, int gy, int64_t wgs, int most
   const int turns = (steps + most - 1) / most, nw = (steps + turns - 1) / turns;
   const hipError_t e = allow_lds_once<AF * 64 + MR>(reinterpret_cast<const void*>(&qgemv_kernel<AF, MR>), kGvMaxLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((qgemv_kernel<AF, MR>), dim3((unsigned)((p.N + 15) / 16), (unsigned)gy), dim3(64 * nw), nw * wave, st, p);
-  return hipGetLastError();
+  return launch_kernel(&qgemv_kernel<AF, MR>, dim3((unsigned)((p.N + 15) / 16), (unsigned)gy), dim3(64 * nw), nw * wave, st, p);
 }
 
 template <int AF>

@@ -322,12 +322,11 @@ static hipError_t launch_fmt(const RnParams& p, int fmt, hipStream_t st) {
   const int64_t wgs = ((int64_t)p.M + ROWS - 1) / ROWS, x = wgs < (1 << 22) ? wgs : (1 << 22);
   const dim3 grid((unsigned)x, (unsigned)((wgs + x - 1) / x)), block(B);
   switch (fmt) {
-    case VDTQ_FMT_INT8: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_INT8, NTL>), grid, block, 0, st, p); break;
-    case VDTQ_FMT_BF16: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_BF16, NTL>), grid, block, 0, st, p); break;
-    case VDTQ_FMT_MXFP4: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP4, NTL>), grid, block, 0, st, p); break;
-    default: hipLaunchKernelGGL((rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP8, NTL>), grid, block, 0, st, p); break;
+    case VDTQ_FMT_INT8: return launch_kernel(&rmsnorm_quantize_kernel<T, C, VDTQ_FMT_INT8, NTL>, grid, block, 0, st, p);
+    case VDTQ_FMT_BF16: return launch_kernel(&rmsnorm_quantize_kernel<T, C, VDTQ_FMT_BF16, NTL>, grid, block, 0, st, p);
+    case VDTQ_FMT_MXFP4: return launch_kernel(&rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP4, NTL>, grid, block, 0, st, p);
+    default: return launch_kernel(&rmsnorm_quantize_kernel<T, C, VDTQ_FMT_MXFP8, NTL>, grid, block, 0, st, p);
   }
-  return hipGetLastError();
 }
 
 // Lanes and vectors of a row: the fewest lanes that hold it in a few vectors

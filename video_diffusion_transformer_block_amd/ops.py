@@ -36,6 +36,15 @@ def _stream(dev: torch.device):
     return ctypes.c_void_p(_raw_stream(dev.index))
 
 
+def _native(r):
+    """The native entry's answer, or the error that it reports as a status
+    (a call that failed in the runtime: making it again could apply it
+    twice)."""
+    if type(r) is int:
+        L.check(r)
+    return r
+
+
 def _launch(fn, dev: torch.device, *args):
     """Calls an entry point with dev current (a launch needs its stream's
     device to be the current one) and the stream as its last argument."""
@@ -440,7 +449,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     if _fast is not None and out is None and fmt in _NORM_FMT:
         r = _fast.norm(x, weight, residual, eps, had_block, _NORM_FMT[fmt], sum_out)
         if r is not None:
-            q, s, total = r
+            q, s, total = _native(r)
             t = INT8Tensor(q, s) if fmt == "int8" else BF16Tensor(q) if fmt == "bf16" else MXTensor(q, s, fmt)
             return t, total
     if not torch.is_tensor(x) or x.dim() != 2:
@@ -497,7 +506,7 @@ def qgemv_w4a16(a: BF16Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = No
     if _fast is not None:
         r = _fast.gemv(0, a.q, None, w.q, w.scales, w.ts, bias, y, out_dtype)
         if r is not None:
-            return r
+            return _native(r)
     M, K = a.q.shape
     N = w.q.shape[0]
     dev = a.q.device
@@ -516,7 +525,7 @@ def qgemv_w4a8(a: INT8Tensor, w: NVFP4Tensor, bias: Optional[torch.Tensor] = Non
     if _fast is not None:
         r = _fast.gemv(1, a.q, a.scales, w.q, w.scales, w.ts, bias, y, out_dtype)
         if r is not None:
-            return r
+            return _native(r)
     M, K = a.q.shape
     N = w.q.shape[0]
     dev = a.q.device
@@ -542,7 +551,7 @@ def qgemv_mx(a: MXTensor, w: MXTensor, bias: Optional[torch.Tensor] = None,
     if _fast is not None and a.fmt in _MX_KIND:
         r = _fast.gemv(_MX_KIND[a.fmt], a.q, a.scales, w.q, w.scales, None, bias, y, out_dtype)
         if r is not None:
-            return r
+            return _native(r)
     M = a.q.shape[0]
     K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
     N = w.q.shape[0]
@@ -569,7 +578,7 @@ def qgemm_mx_grouped(a: MXTensor, w: MXTensor, offsets: torch.Tensor, bias: Opti
     if _fast is not None and a.fmt in _MX_KIND:
         r = _fast.grouped(a.fmt == "mxfp8", a.q, a.scales, w.q, w.scales, offsets, bias, y, out_dtype)
         if r is not None:
-            return r
+            return _native(r)
     T = a.q.shape[0]
     K = a.q.shape[1] * (2 if a.fmt == "mxfp4" else 1)
     dev = a.q.device
