@@ -418,6 +418,14 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * (qgemv_mx too: unlike qgemm_mx, it does not use the block-scaled matrix
  * instruction, whose E4M3 x E2M1 sums drop low bits).
  *
+ * Range of qgemv_mx: an element times its block's scale becomes a bf16 value.
+ * That is exact for scale bytes 3 .. 246 of E4M3 and 0 .. 252 of E2M1
+ * elements, whatever the codes, and so for all blocks that encode finite fp32
+ * values of 2^-116 and above.  Under lower bytes (E4M3: 0, 1, 2) bits below
+ * 2^-133 are rounded away; an element that reaches 2^128 (bytes above 246 /
+ * 252) becomes an infinity, also where qgemm_mx would give a finite product
+ * with a small scale of the other operand.
+ *
  * Defined by: [gist] §4 / [yly] §四 (4-bit weights in every linear), with
  * the activations of [gist] §2.A and §2.C.
  *
@@ -457,7 +465,8 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  * Defined by: [gist] §2.A / §3.1 and §4 as for qgemm_mx.
  *
  * Products and sums: fp32 output, and bf16 output of MXFP4 activations: exact
- * products, added in fp32.  bf16 output of MXFP8 activations: as qgemm_mx, the
+ * products, added in fp32 (fp32 output of MXFP8 activations: over the range of
+ * scales of qgemv_mx).  bf16 output of MXFP8 activations: as qgemm_mx, the
  * block-scaled matrix instruction, which cuts each of 8 consecutive products
  * at 2^-13 of the power of two below the largest of them (3.4e-5 of the
  * result's norm on typical rows; half a bf16 step is 2e-3).

@@ -245,7 +245,8 @@ struct MgTile {
 // workgroup slot.
 //
 // EXACT (MXFP8 rows, fp32 output): the fragments are decoded to bf16 (every
-// element times its block's power of two is exact) for
+// element times its block's power of two is exact over the scales that
+// qgemv.hip states) for
 // v_mfma_f32_32x32x16_bf16, which does not cut products against each other.
 // A lane then holds whole blocks of 32: step s, half l / 32: block 2 s + l / 32.
 template <bool A8, int BM, int BN, int NS, bool EXACT = false, int WGS = MgTile<A8, BM, BN, NS>::WGS>

@@ -7,7 +7,10 @@
 // G = 32 (MXFP4).  Operands are decoded exactly and multiplied by
 // v_mfma_f32_16x16x32, whose products are exact and whose sums are fp32:
 //   bf16 and MX activations: in bf16 (E2M1 x E4M3 has at most 6 significant
-//     bits, E4M3 4, E8M0 is a power of two that the conversion applies);
+//     bits, E4M3 4, E8M0 is a power of two that the conversion applies: exact
+//     while the value is a bf16 one, subnormals (multiples of 2^-133) among
+//     them, which both the conversion and the matrix instruction keep; so for
+//     scale bytes 3 .. 246 of E4M3 and 0 .. 252 of E2M1 codes);
 //   INT8 activations: in fp16 (7 bits; E2M1 x E4M3 is 2^-10 .. 2688), whose
 //     packed multiply decodes NVFP4 in half the instructions.
 // The block-scaled matrix instruction is not used here: with E4M3 operands it
