@@ -433,10 +433,11 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); with K a
  * multiple of 128 the scales are 8-byte (NVFP4) or 4-byte (MX) aligned, else
  * they need no alignment; N * K / 2 has no limit below the memory's.
- * No workspace.  A NaN in an activation row, in its scale (INT8) or an
+ * No workspace.  y may not share memory with an operand (refused).
+ * A NaN in an activation row, in its scale (INT8) or an
  * 0xFF scale byte (MX) makes that row of Y NaN and no other.
  * Errors: VDTQ_EINVAL for null or misaligned pointers, bad sizes or
- * formats, ldy < N; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS,
+ * formats, ldy < N, y over an operand; VDTQ_EUNSUPPORTED for M > VDTQ_GEMV_MAX_ROWS,
  * K > 2^24 or N >= 2^26.
  */
 #define VDTQ_GEMV_MAX_ROWS 32
@@ -484,9 +485,9 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev,
  *                offsets[E] on are left as they were
  * T, N, E        >= 0 (T, N or E of 0 is a no-op); E <= 65536
  * K              > 0, multiple of 32
- * No workspace.
+ * No workspace.  y may not share memory with an operand (refused).
  * Errors: VDTQ_EINVAL for a bad a_fmt or size, null or misaligned pointers,
- * ldy < N; VDTQ_EUNSUPPORTED for K not a multiple of 128, K > 2^24,
+ * ldy < N, y over an operand; VDTQ_EUNSUPPORTED for K not a multiple of 128, K > 2^24,
  * N >= 2^26, T > 2^30 or more output tiles than a launch holds (2^24 of 256
  * rows of an expert x 256 features; of 64 x 128 with MXFP8 and fp32 output or
  * weights of an expert of 4 GB or more).

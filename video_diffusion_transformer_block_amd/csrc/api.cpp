@@ -4,6 +4,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "../../include/vdtq.h"
@@ -343,6 +344,28 @@ static int small_check(const char* name, const void* a_q, const void* a_s, const
   return VDTQ_OK;
 }
 
+// An operand: its first byte and its length.
+struct Operand {
+  const void* p;
+  int64_t bytes;
+};
+
+// Whether a row of y shares a byte with an operand: workgroups store their
+// columns of y while others still read the operands.  An operand between two
+// rows of a strided y is none of it.
+static bool y_overlaps(const void* y, int64_t ldy, int out_dtype, int64_t M, int64_t N, std::initializer_list<Operand> ops) {
+  const uintptr_t es = out_dtype == VDTQ_OUT_F32 ? 4 : 2, row = (uintptr_t)N * es, stride = (uintptr_t)ldy * es;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(y), end = a + (uintptr_t)(M - 1) * stride + row;
+  for (const Operand& o : ops) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(o.p), n = (uintptr_t)o.bytes;
+    if (!o.p || n == 0 || b >= end || b + n <= a) continue;
+    const uintptr_t d = b < a ? 0 : (b - a) % stride;      // past the start of the row before it
+    if (d < row || d + n > stride) return true;
+  }
+  return false;
+}
+static int overlap_error(const char* name) { return fail(VDTQ_EINVAL, "%s: y overlaps an operand", name); }
+
 // The further checks of the few-row products.  With K a multiple of 128 every
 // row's scales start on 8 (NVFP4) or 4 bytes (MX) if the first ones do.
 static int gemv_check(const char* name, int64_t M, int64_t K, const void* w_s, const void* a_s, int run) {
@@ -361,6 +384,9 @@ int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev, const uint8_t* w_s_de
   if (rc || (rc = gemv_check(name, M, K, w_s_dev, nullptr, 8))) return rc;
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned w_ts", name);
+  if (y_overlaps(y_dev, ldy, out_dtype, M, N, {{a_dev, 2 * M * K}, {w_q_dev, N * (K / 2)}, {w_s_dev, N * (K / 16)},
+                                               {w_ts_dev, 8}, {bias_dev, 4 * N}}))
+    return overlap_error(name);
   hipError_t e = vdtq::launch_qgemv(0, a_dev, nullptr, w_q_dev, w_s_dev, w_ts_dev, bias_dev, y_dev, ldy, out_dtype, M,
                                     N, K, static_cast<hipStream_t>(stream));
   return hip_status(e, "qgemv_w4a16 launch");
@@ -375,6 +401,9 @@ int qgemv_w4a8(const int8_t* a_q_dev, const float* a_s_dev, const uint8_t* w_q_d
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4) || !aligned(a_s_dev, 4))
     return fail(VDTQ_EINVAL, "%s: null w_ts or misaligned w_ts / a_s", name);
+  if (y_overlaps(y_dev, ldy, out_dtype, M, N, {{a_q_dev, M * K}, {a_s_dev, 4 * M}, {w_q_dev, N * (K / 2)},
+                                               {w_s_dev, N * (K / 16)}, {w_ts_dev, 8}, {bias_dev, 4 * N}}))
+    return overlap_error(name);
   hipError_t e = vdtq::launch_qgemv(1, a_q_dev, a_s_dev, w_q_dev, w_s_dev, w_ts_dev, bias_dev, y_dev, ldy, out_dtype,
                                     M, N, K, static_cast<hipStream_t>(stream));
   return hip_status(e, "qgemv_w4a8 launch");
@@ -388,6 +417,9 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, const ui
   int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 32);
   if (rc || (rc = gemv_check(name, M, K, w_s_dev, a_s_dev, 4))) return rc;
   if (M == 0 || N == 0) return ok();
+  if (y_overlaps(y_dev, ldy, out_dtype, M, N, {{a_q_dev, M * (a_fmt == VDTQ_FMT_MXFP8 ? K : K / 2)}, {a_s_dev, M * (K / 32)},
+                                               {w_q_dev, N * (K / 2)}, {w_s_dev, N * (K / 32)}, {bias_dev, 4 * N}}))
+    return overlap_error(name);
   hipError_t e = vdtq::launch_qgemv(a_fmt == VDTQ_FMT_MXFP8 ? 2 : 3, a_q_dev, a_s_dev, w_q_dev, w_s_dev, nullptr,
                                     bias_dev, y_dev, ldy, out_dtype, M, N, K, static_cast<hipStream_t>(stream));
   return hip_status(e, "qgemv_mx launch");
@@ -410,6 +442,10 @@ int qgemm_mx_grouped(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, 
   const bool small = (a_fmt == VDTQ_FMT_MXFP8 && out_dtype == VDTQ_OUT_F32) || !vdtq::grouped_256_fits(N, K);
   if (!vdtq::grouped_tiles_fit(T, E, N, small ? 64 : 256, small ? 128 : 256))
     return fail(VDTQ_EUNSUPPORTED, "%s: too many output tiles", name);
+  if (y_overlaps(y_dev, ldy, out_dtype, T, N, {{a_q_dev, T * (a_fmt == VDTQ_FMT_MXFP8 ? K : K / 2)}, {a_s_dev, T * (K / 32)},
+                                               {w_q_dev, E * N * (K / 2)}, {w_s_dev, E * N * (K / 32)},
+                                               {bias_dev, 4 * E * N}, {offsets_dev, 4 * (E + 1)}}))
+    return overlap_error(name);
   const vdtq::MxGrouped q{a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, offsets_dev, y_dev, ldy,
                           (int32_t)T, (int32_t)N, (int32_t)K, (int32_t)E, out_dtype == VDTQ_OUT_F32};
   hipError_t e = vdtq::launch_qgemm_mx_grouped(a_fmt == VDTQ_FMT_MXFP8, q, static_cast<hipStream_t>(stream));
