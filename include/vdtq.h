@@ -430,9 +430,8 @@ int rmsnorm_quantize(const void* x_dev, int64_t M, int64_t K, int64_t ldx,
  * the activations of [gist] §2.A and §2.C.
  *
  * Operands as for the call of the same name, except: M <=
- * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); with K a
- * multiple of 128 the scales are 8-byte (NVFP4) or 4-byte (MX) aligned, else
- * they need no alignment; N * K / 2 has no limit below the memory's.
+ * VDTQ_GEMV_MAX_ROWS; K any positive multiple of 16 (qgemv_mx: 32); block
+ * scales need no alignment; N * K / 2 has no limit below the memory's.
  * No workspace.  y may not share memory with an operand (refused).
  * A NaN in an activation row, in its scale (INT8) or an
  * 0xFF scale byte (MX) makes that row of Y NaN and no other.

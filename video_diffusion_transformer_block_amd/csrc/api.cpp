@@ -366,13 +366,11 @@ static bool y_overlaps(const void* y, int64_t ldy, int out_dtype, int64_t M, int
 }
 static int overlap_error(const char* name) { return fail(VDTQ_EINVAL, "%s: y overlaps an operand", name); }
 
-// The further checks of the few-row products.  With K a multiple of 128 every
-// row's scales start on 8 (NVFP4) or 4 bytes (MX) if the first ones do.
-static int gemv_check(const char* name, int64_t M, int64_t K, const void* w_s, const void* a_s, int run) {
+// The further check of the few-row products (block scales need no alignment:
+// the kernels read them in runs of any).
+static int gemv_check(const char* name, int64_t M) {
   if (M > VDTQ_GEMV_MAX_ROWS)
     return fail(VDTQ_EUNSUPPORTED, "%s: M=%lld is more than %d rows", name, (long long)M, VDTQ_GEMV_MAX_ROWS);
-  if (K % 128 == 0 && (!aligned(w_s, run) || !aligned(a_s, run)))
-    return fail(VDTQ_EINVAL, "%s: scales need %d bytes alignment", name, run);
   return VDTQ_OK;
 }
 
@@ -381,7 +379,7 @@ int qgemv_w4a16(const void* a_dev, const uint8_t* w_q_dev, const uint8_t* w_s_de
                 void* stream) {
   const char* name = "qgemv_w4a16";
   int rc = small_check(name, a_dev, a_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
-  if (rc || (rc = gemv_check(name, M, K, w_s_dev, nullptr, 8))) return rc;
+  if (rc || (rc = gemv_check(name, M))) return rc;
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4)) return fail(VDTQ_EINVAL, "%s: null or misaligned w_ts", name);
   if (y_overlaps(y_dev, ldy, out_dtype, M, N, {{a_dev, 2 * M * K}, {w_q_dev, N * (K / 2)}, {w_s_dev, N * (K / 16)},
@@ -397,7 +395,7 @@ int qgemv_w4a8(const int8_t* a_q_dev, const float* a_s_dev, const uint8_t* w_q_d
                int64_t N, int64_t K, void* stream) {
   const char* name = "qgemv_w4a8";
   int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 16);
-  if (rc || (rc = gemv_check(name, M, K, w_s_dev, nullptr, 8))) return rc;
+  if (rc || (rc = gemv_check(name, M))) return rc;
   if (M == 0 || N == 0) return ok();
   if (!w_ts_dev || !aligned(w_ts_dev, 4) || !aligned(a_s_dev, 4))
     return fail(VDTQ_EINVAL, "%s: null w_ts or misaligned w_ts / a_s", name);
@@ -415,7 +413,7 @@ int qgemv_mx(int a_fmt, const uint8_t* a_q_dev, const uint8_t* a_s_dev, const ui
   const char* name = "qgemv_mx";
   if (a_fmt != VDTQ_FMT_MXFP4 && a_fmt != VDTQ_FMT_MXFP8) return fail(VDTQ_EINVAL, "%s: a_fmt=%d", name, a_fmt);
   int rc = small_check(name, a_q_dev, a_s_dev, w_q_dev, w_s_dev, bias_dev, y_dev, ldy, out_dtype, M, N, K, 32);
-  if (rc || (rc = gemv_check(name, M, K, w_s_dev, a_s_dev, 4))) return rc;
+  if (rc || (rc = gemv_check(name, M))) return rc;
   if (M == 0 || N == 0) return ok();
   if (y_overlaps(y_dev, ldy, out_dtype, M, N, {{a_q_dev, M * (a_fmt == VDTQ_FMT_MXFP8 ? K : K / 2)}, {a_s_dev, M * (K / 32)},
                                                {w_q_dev, N * (K / 2)}, {w_s_dev, N * (K / 32)}, {bias_dev, 4 * N}}))
