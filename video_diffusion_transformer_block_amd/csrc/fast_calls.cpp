@@ -178,6 +178,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
+  if (b != (int)b) Py_RETURN_NONE;
   int64_t M, K;
   int dev;
   if (!shape2(a[0], M, K, dev)) Py_RETURN_NONE;

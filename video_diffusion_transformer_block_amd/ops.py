@@ -461,6 +461,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         raise ValueError(f"fmt {fmt!r}")
     if K % 16 or (fmt in ("mxfp4", "mxfp8") and K % 32):
         raise ValueError(f"K = {K} is not a multiple of {32 if fmt in ('mxfp4', 'mxfp8') else 16}")
+    if not -2 ** 31 <= had_block < 2 ** 31:       # the library's int would drop the upper bits
+        raise ValueError(f"had_block = {had_block}")
     if weight is not None:
         _buf(weight, "weight", torch.float32, (K,), dev)
     ldr = lds = 0
