@@ -33,7 +33,7 @@ typedef int mg_int4 __attribute__((ext_vector_type(4)));
 typedef int mg_int8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMgStep = 512;                    // K of a wavefront
-constexpr int kMgMaxWaves = 14;                 // more do not fit the LDS
+constexpr int kMgMaxWaves = 14;                 // 148 KB of the 160 KB LDS (15 would fit, 16 not; 15 not measured)
 constexpr int kMgCodes = 16 * kMgStep / 2;      // a block of a wavefront: codes, then
 constexpr int kMgSlot = kMgCodes + 256;         // 16 scale bytes of 16 features
 constexpr int kMgLoads = kMgCodes / 1024 + 1;
@@ -241,8 +241,9 @@ struct MgTile {
 
 // 1111 rows over 16 experts, 3072 -> 1920, MXFP8: 20 us for 58 MB and 13 GFLOP
 // (tiles of 256 x 256 took 41, of 128 x 128 26); what bounds it is the depth of
-// one tile (24 stages and the first loads' latency) with about 1.5 tiles a
-// workgroup slot.
+// one tile (24 stages and the first loads' latency): its 360 tiles are 1.4 a
+// compute unit, less than half of the 768 workgroups that could run at once, so
+// little passes under another's matrix instructions here.
 //
 // EXACT (MXFP8 rows, fp32 output): the fragments are decoded to bf16 (every
 // element times its block's power of two is exact over the scales that

@@ -176,8 +176,9 @@ struct GvStep {
   // activations go to LDS decoded to 16 bits where they are few (every
   // fragment then needs no decoding: 11.0 -> 10.2 us for one INT8 row,
   // K = 3072, N = 12288), as they are from 16 rows on, where that would
-  // double the LDS and leave room for fewer wavefronts (64 rows over 32
-  // experts, K = 1920, N = 7680: 52 -> 70 us)
+  // double the LDS and leave room for fewer wavefronts (52 -> 70 us for 64
+  // rows over 32 experts, 25 of them hit, K = 1920, N = 7680, bf16 output, which
+  // now has a kernel of its own)
   static constexpr bool DECODED = AF == kActBf16 || MR == 4;
   static constexpr int KS = MR == 4 || (MR == 16 && AF != kActBf16) ? 512 : 256;   // K
   static constexpr int WAVES = MR == 32 ? 8 : 16;                      // at most
@@ -442,7 +443,7 @@ hipError_t launch_qgemm_mx_grouped_exact(const MxGrouped& q, hipStream_t st) {
   p.w_q = q.w_q; p.w_s = q.w_s; p.bias = q.bias; p.offsets = q.offsets;
   p.y = q.y; p.ldy = q.ldy; p.out_f32 = q.out_f32;
   p.M = q.T; p.N = q.N; p.K = q.K; p.E = q.E;
-  // 8 a unit: 64 rows over 32 experts, K = 1920, N = 7680: 78 us, 94 with 4;
+  // 8 a unit: 64 rows over 32 experts, 2 each, K = 1920, N = 7680: 78 us, 94 with 4;
   // half the LDS each and 4 feature tiles one after the other took 108 (2 rows
   // over 20 experts, K = 4992, N = 4619: 13.4 and 21.8)
   const int64_t wgs = (int64_t)((q.N + 15) / 16) * std::min(q.E, q.T);
